@@ -404,6 +404,50 @@ MOE_API moe_status_t moe_expert_ffn_rows(const moe_shape_t* shape, int64_t rows_
                                          const void* x_rows, const void* W1, const void* b1, const void* W2,
                                          const void* b2, float* y, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ---- the experts' parts: grouped matrix products ---------------------------------------------------
+ * The products of the expert FFN on their own, for experts that moe_expert_ffn does not have (gated
+ * ones, other widths, adapters) and for training them.  Rows are grouped by expert as moe_permute
+ * leaves them: expert e owns rows [offsets[e], offsets[e+1]), any number of them, also none.
+ * The library keeps no state and needs no workspace for these calls, so any number of them may run at
+ * once; they may be captured into CUDA graphs.  The device that owns the buffers must be current. */
+typedef struct {
+  int32_t E;             /* experts, 1..256 */
+  int64_t rows_cap;      /* rows that x and y hold, >= offsets[E]; < 2^31 - 1024 */
+  int32_t K;             /* contraction of the forward product */
+  int32_t N;             /* output columns of the forward product */
+  moe_dtype_t dtype;     /* storage type of x, W, bias (and of dy) */
+  moe_dtype_t out_dtype; /* storage type of y; the products are summed in fp32 and rounded once */
+  int32_t transpose_w;   /* 0: W[E,K,N] (the layout of W1 and W2); 1: W[E,N,K] */
+  int64_t ldx;           /* elements between rows of x; 0 = K (contiguous) */
+  int64_t ldy;           /* elements between rows of y (dy); 0 = N */
+} moe_matmul_t;
+
+/* y[r,n] = sum_k x[r,k] * W[e,k,n] + bias[e,n] for every row r of expert e (transpose_w = 1: W[e,n,k]).
+ * With transpose_w = 1 and the forward's W this is the data gradient: x = dy[rows,N_fwd], K = N_fwd,
+ * N = K_fwd.  x[rows_cap, ldx], W, y[rows_cap, ldy] and bias[E,N] (or NULL) are device buffers; y must
+ * not overlap the inputs.  offsets[E+1] is a device int32 array, non-decreasing from 0, offsets[E] <=
+ * rows_cap; entries that break this are clamped on the device, so no row outside [0, rows_cap) is read
+ * or written, and recorded in status.  Rows of y in [offsets[E], rows_cap), and columns [N, ldy), are
+ * left as they were.  status: an optional (NULL) device int32, 4-byte aligned and 0 before its first
+ * use, where a bad offset or a bounded wait that ran out is recorded for moe_get_device_status.
+ * bf16: tcgen05 tensor cores; fp32: CUDA cores.  Each y element is one sum in a fixed order.
+ * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers - 16 bytes, offsets and status 4 - E
+ * outside [1, 256], rows_cap < 0, K or N < 1, ld below the row length, unknown types);
+ * MOE_ERR_UNSUPPORTED (bf16: K, N, ldx or ldy not a multiple of 8; fp32: of 4; rows_cap
+ * >= 2^31 - 1024, N > 4194240 or more than 2^31 output tiles; fp32 x with a bf16 y: bf16 x takes either
+ * y, fp32 x only an fp32 y); MOE_ERR_CUDA.  rows_cap = 0 launches nothing.  1 launch. */
+MOE_API moe_status_t moe_grouped_matmul(const moe_matmul_t* m, const int32_t* offsets, const void* x, const void* W,
+                                        const void* bias, void* y, int32_t* status, cudaStream_t stream);
+
+/* Weight gradient of the product: dW[e,k,n] = sum over the rows r of expert e of x[r,k] * dy[r,n], and
+ * with db not NULL the bias gradient db[e,n] = sum_r dy[r,n].  x[rows_cap, ldx] and dy[rows_cap, ldy]
+ * are in m->dtype; dW[E,K,N] and db[E,N] are fp32, contiguous, 16-byte aligned, and overwritten: an
+ * expert without rows gets zeros.  out_dtype and transpose_w are not used (for a W[E,N,K] pass dy as x
+ * and x as dy).  Sums run in a fixed order: the same inputs give the same bits.  Rows, offsets, status,
+ * checks and errors as above; rows_cap = 0 writes zeros.  1 launch, 1 more with db. */
+MOE_API moe_status_t moe_grouped_wgrad(const moe_matmul_t* m, const int32_t* offsets, const void* x, const void* dy,
+                                       float* dW, float* db, int32_t* status, cudaStream_t stream);
+
 /* Kernel-selection switches for side-by-side comparisons of the kernels; normal use needs none.
  *   MOE_KERNEL_NO_CTA_PAIR  single-CTA 128-row grouped-GEMM tiles everywhere, instead of the CTA-pair
  *                           256 x 256 tiles the long-segment shapes use (forward and backward GEMMs)

@@ -29,7 +29,7 @@ ENTRY_POINTS = (
     "moe_last_launch_count", "moe_status_string", "moe_route_noalloc", "moe_capacity",
     "moe_train_workspace_size", "moe_forward_train", "moe_backward", "moe_loss_sums", "moe_losses_from_sums",
     "moe_set_kernel_options", "moe_get_kernel_options", "moe_copy_row_segments", "moe_expert_ffn_rows",
-    "moe_expert_ffn_rows_workspace_size", "moe_debug_activation",
+    "moe_expert_ffn_rows_workspace_size", "moe_debug_activation", "moe_grouped_matmul", "moe_grouped_wgrad",
 )
 MOE_KERNEL_DEFAULT, MOE_KERNEL_NO_CTA_PAIR, MOE_KERNEL_NO_TC_GATE, MOE_KERNEL_NO_TMA_ROUTER = 0, 1, 2, 4
 
@@ -60,6 +60,13 @@ class WsView(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("status", "offsets", "cnt_pre", "row_of", "row_token", "row_slot",
                                                "x_perm", "h", "y")] + [("bytes", ctypes.c_size_t),
                                                                         ("scores", ctypes.c_void_p)]
+
+
+class Matmul(ctypes.Structure):
+    """moe_matmul_t: sizes, types and row pitches of a product grouped by expert."""
+    _fields_ = [("E", ctypes.c_int32), ("rows_cap", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("transpose_w", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
 class RowSegment(ctypes.Structure):
@@ -119,6 +126,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_expert_ffn_rows_workspace_size.restype = sz
     lib.moe_expert_ffn_rows.argtypes = [P(Shape), ctypes.c_int64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_expert_ffn_rows.restype = st
+    lib.moe_grouped_matmul.argtypes = [P(Matmul), vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_grouped_matmul.restype = st
+    lib.moe_grouped_wgrad.argtypes = [P(Matmul), vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_grouped_wgrad.restype = st
     lib.moe_debug_activation.argtypes = [ctypes.c_int, vp, vp, ctypes.c_int64, vp]
     lib.moe_debug_activation.restype = st
     lib.moe_debug_timeout_probe.argtypes = [vp, sz, vp]
@@ -268,6 +279,14 @@ def moe_expert_ffn_rows(shape, rows_cap, offsets, x_rows, W1, b1, W2, b2, y, ws,
                                               ws_bytes, stream)
 
 
+def moe_grouped_matmul(m: Matmul, offsets, x, W, bias, y, status=None, stream=0) -> int:
+    return load_library().moe_grouped_matmul(ctypes.byref(m), offsets, x, W, bias, y, status, stream)
+
+
+def moe_grouped_wgrad(m: Matmul, offsets, x, dy, dW, db=None, status=None, stream=0) -> int:
+    return load_library().moe_grouped_wgrad(ctypes.byref(m), offsets, x, dy, dW, db, status, stream)
+
+
 def moe_debug_activation(activation: int, u, out, n: int, stream=0) -> int:
     return load_library().moe_debug_activation(int(activation), u, out, int(n), stream)
 
@@ -408,3 +427,16 @@ class MoEBuffers:
         g = Grad(dout.data_ptr(), float(d_aux), float(d_z), p("dx"), p("dWg"), p("dbg"), p("dW1"), p("db1"), p("dW2"),
                  p("db2"), p("dw"))
         return _check(moe_backward(self.shape, self.io, g, self.ws_ptr, self.ws_bytes, self.stream()), "moe_backward")
+
+
+# The operators on torch tensors, imported on first use: the binding itself loads without torch.
+_OPERATORS = ("grouped_matmul", "grouped_wgrad")
+
+
+def __getattr__(name):
+    if name in _OPERATORS:
+        from . import operators
+
+        globals()[name] = value = getattr(operators, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

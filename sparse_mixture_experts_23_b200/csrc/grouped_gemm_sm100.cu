@@ -8,6 +8,8 @@
 //   GEMM1 (EPI_SILU):     the same with SiLU (Mixtral block experts); b1 and b2 may be absent (zero)
 //   GEMM2 (EPI_COMBINE):  out[t, n] += w(t,s) * ( sum_k h[r,k] W2[e,k,n] + b2[e,n] ),  t,s = row r's
 //   GEMM2 (EPI_STORE_Y):  y[r, n]   = sum_k h[r,k] W2[e,k,n] + b2[e,n]
+//   moe_grouped_matmul (EPI_ROWS_F32, EPI_ROWS_BF16): the same sum with any N and K that are multiples of 8, rows of
+//   x and y at a pitch of their own, and caller-given offsets
 //
 // Design (one persistent CTA per SM, 64 + 32 * kEpiWarps threads: 192 with the default 4 epilogue warps):
 //   warp 0      TMA producer: A tile [128 rows x 64 k] (K-major, 128B swizzle) and B tile
@@ -34,6 +36,7 @@
 #include <stdlib.h>
 
 #include "moe_internal.cuh"
+#include "segments.cuh"
 #include "sm100_ptx.cuh"
 
 namespace moe {
@@ -58,11 +61,14 @@ enum {
   EPI_SILU = 3,
   EPI_DGRAD_GELU = 4,
   EPI_DGRAD_SILU = 5,
-  EPI_ROUTER = 6  // the gate: softmax, top-k, renormalised weights and a chunk's loss partials
+  EPI_ROUTER = 6,  // the gate: softmax, top-k, renormalised weights and a chunk's loss partials
+  EPI_ROWS_F32 = 7,  // the plain product with its bias, rows at pitch ldo, columns past N masked
+  EPI_ROWS_BF16 = 8
 };
 // GEMM1 epilogues write h = act(acc + b1); GEMM2 epilogues combine or store y; the backward's
 // first GEMM (G = dout_rows . W2[e]^T) writes du = w * G * act'(u) and accumulates dw = G . h.
 __host__ __device__ constexpr bool epi_h(int epi) { return epi == EPI_GELU || epi == EPI_SILU; }
+__host__ __device__ constexpr bool epi_rows(int epi) { return epi == EPI_ROWS_F32 || epi == EPI_ROWS_BF16; }
 __host__ __device__ constexpr bool epi_dgrad(int epi) { return epi == EPI_DGRAD_GELU || epi == EPI_DGRAD_SILU; }
 
 template <int BN>
@@ -122,6 +128,9 @@ struct GemmArgs {
   // MMA warp runs that tile's main loop (the forward's out, which GEMM2 then accumulates into)
   float4* clear;
   long long clear_n;
+  // EPI_ROWS_*: offsets are the caller's (clamped to [0, rows_cap] here); output rows are ldo elements apart
+  long long rows_cap;
+  long long ldo;
 };
 
 using namespace sm100;
@@ -213,7 +222,7 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const uint32_t
     mine[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
                           __uint_as_float(r[4 * q + 3]));
   __syncwarp();
-  const float bj = brow ? __bfloat162float(brow[n0 + lane]) : 0.f;
+  const float bj = brow && (EPI != EPI_ROWS_F32 || n0 + lane < g.N) ? __bfloat162float(brow[n0 + lane]) : 0.f;
   const int nr = nrows < 32 ? nrows : 32;
   // 8 rows at a time: their values (and activations) are independent, so the latency of one row's
   // chain overlaps the others' (one warp per SM sub-partition runs this loop)
@@ -238,6 +247,8 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const uint32_t
         const int tok = __shfl_sync(0xffffffffu, my_tok, i);
         const float w = __shfl_sync(0xffffffffu, my_w, i);
         if (ok) atomicAdd(g.out + (size_t)tok * g.N + n0 + lane, w * v[q]);
+      } else if (EPI == EPI_ROWS_F32) {
+        if (ok && n0 + lane < g.N) g.y[(size_t)(grow0 + off) * g.ldo + n0 + lane] = v[q];
       } else {
         if (ok) g.y[(size_t)(grow0 + off) * g.N + n0 + lane] = v[q];
       }
@@ -310,6 +321,43 @@ __device__ __forceinline__ void epilogue_h_rows(const GemmArgs& g, const uint32_
     dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
     if (urow) urow[j] = make_uint4(uw[0], uw[1], uw[2], uw[3]);
   }
+}
+
+// EPI_ROWS_BF16: a 64-column group of a warp's 32 rows (lane i owns tile row i), y = bf16(acc + bias).  The
+// values pass through the warp's staging box in the same swizzle (16-byte piece j of row i at j ^ (i % 8):
+// writes and reads are free of bank conflicts), so that 8 lanes store one row's 128 contiguous bytes.  Row i
+// is output row grow0 + off_i as in epilogue_chunk; rows past the segment and columns past N (multiples of
+// 8: whole pieces) are skipped.  The rounding to bf16 is the output type's own, once, after the bias.
+template <bool SPREAD>
+__device__ __forceinline__ void epilogue_rows_bf16(const GemmArgs& g, const uint32_t (&r0)[32], const uint32_t (&r1)[32],
+                                                   uint8_t* stg, int lane, int grow0, int nrows,
+                                                   const __nv_bfloat16* brow, int n0) {
+  uint8_t* row = stg + lane * 128;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t* src = j < 4 ? &r0[8 * j] : &r1[8 * (j - 4)];
+    const uint4 bb = n0 + 8 * j < g.N ? bias8(brow, n0 + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+    const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&bb);
+    uint32_t w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float2 f = __bfloat1622float2(b2[u]);
+      const __nv_bfloat162 v =
+          __floats2bfloat162_rn(__uint_as_float(src[2 * u]) + f.x, __uint_as_float(src[2 * u + 1]) + f.y);
+      w[u] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+  const int piece = lane & 7, n = n0 + 8 * piece;
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int i = 4 * p + (lane >> 3);
+    const int off = SPREAD ? 32 * (i >> 3) + (i & 7) : i;
+    const uint4 v = *reinterpret_cast<const uint4*>(stg + i * 128 + ((piece ^ (i & 7)) * 16));
+    if (off < nrows && n < g.N) *reinterpret_cast<uint4*>(g.h_out + (size_t)(grow0 + off) * g.ldo + n) = v;
+  }
+  __syncwarp();
 }
 
 // Backward epilogue of 32 accumulator columns of one row (lane = row): G = acc is the row's
@@ -494,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* prefix = offs + 260;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int E = g.E, NT = g.N / BN, KB = g.K / BK;
+  const int E = g.E, NT = (g.N + BN - 1) / BN, KB = (g.K + BK - 1) / BK;
   float* stg = reinterpret_cast<float*>(smem + C::kStgOff + (warp >= 2 ? warp - 2 : 0) * kStgWarpBytes);
 
   if (threadIdx.x == 0) {
@@ -513,10 +561,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
   }
-  for (int i = threadIdx.x; i <= E; i += kThreads) offs[i] = g.offsets ? g.offsets[i] : (i == 0 ? 0 : g.single_rows);
+  if constexpr (epi_rows(EPI)) {
+    if (warp == 0) load_segments(g.offsets, E, g.rows_cap, BM, NT, offs, prefix, g.status, blockIdx.x == 0);
+  } else {
+    for (int i = threadIdx.x; i <= E; i += kThreads) offs[i] = g.offsets ? g.offsets[i] : (i == 0 ? 0 : g.single_rows);
+  }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (!epi_rows(EPI) && threadIdx.x == 0) {
     int run = 0;
     for (int e = 0; e < E; ++e) {
       prefix[e] = run;
@@ -676,9 +728,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (half == 0 && wrows > 0)
           router_epilogue<BN>(g, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN), stg, lane,
                               row0 + quarter * 32, wrows);
+      } else if constexpr (EPI == EPI_ROWS_BF16) {
+#pragma unroll 1
+        for (int c = half * kChunks; c < (half + 1) * kChunks; c += 2) {
+          const int n0 = n_idx * BN + c * 32;
+          if (wrows <= 0 || n0 >= g.N) break;
+          uint32_t r0[32], r1[32];
+          const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN + c * 32);
+          tmem_ld32(taddr, r0);
+          tmem_ld32(taddr + 32, r1);
+          if (spread) epilogue_rows_bf16<true>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, row0 + wbase, wrows, brow, n0);
+          else epilogue_rows_bf16<false>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, row0 + wbase, wrows, brow, n0);
+        }
       } else
 #pragma unroll 1
       for (int c = half * kChunks; c < (half + 1) * kChunks; ++c) {
+        if (epi_rows(EPI) && n_idx * BN + c * 32 >= g.N) break;
         uint32_t r[32];
         tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN + c * 32), r);
         if constexpr (epi_dgrad(EPI)) {
@@ -791,7 +856,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
-  const int E = g.E, NT = g.N / C::kTileN, KB = g.K / C::kStageK;
+  const int E = g.E, NT = (g.N + C::kTileN - 1) / C::kTileN, KB = (g.K + C::kStageK - 1) / C::kStageK;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -808,10 +873,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
   }
-  for (int i = threadIdx.x; i <= E; i += kThreads) offs[i] = g.offsets[i];
+  if constexpr (epi_rows(EPI)) {
+    if (warp == 0) load_segments(g.offsets, E, g.rows_cap, C::kTileM, NT, offs, prefix, g.status, blockIdx.x == 0);
+  } else {
+    for (int i = threadIdx.x; i <= E; i += kThreads) offs[i] = g.offsets[i];
+  }
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), C::kTmemCols);
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (!epi_rows(EPI) && threadIdx.x == 0) {
     int run = 0;
     for (int e = 0; e < E; ++e) {
       prefix[e] = run;
@@ -982,6 +1051,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             epilogue_h_box<EPI>(&tmC, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, brow, n0, wrow0, g.u_out, g.N);
           else if (wrows > 0) epilogue_h_rows<EPI>(g, r0, r1, lane, wrows, brow, n0, wrow0);
         }
+      } else if constexpr (EPI == EPI_ROWS_BF16) {
+#pragma unroll 1
+        for (int c = half * nch; c < (half + 1) * nch; c += 2) {
+          const int n0 = n_idx * C::kTileN + colbase + c * 32;
+          if (wrows <= 0 || n0 >= g.N) break;
+          uint32_t r0[32], r1[32];
+          tmem_ld32(taddr + c * 32, r0);
+          tmem_ld32(taddr + (c + 1) * 32, r1);
+          epilogue_rows_bf16<false>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, wrow0, wrows, brow, n0);
+        }
       } else if constexpr (epi_dgrad(EPI)) {
         float dw = 0.f;
 #pragma unroll 1
@@ -994,6 +1073,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
 #pragma unroll 1
         for (int c = half * nch; c < (half + 1) * nch; ++c) {
+          if (epi_rows(EPI) && n_idx * C::kTileN + colbase + c * 32 >= g.N) break;
           uint32_t r[32];
           tmem_ld32(taddr + c * 32, r);
           if (wrows > 0)
@@ -1051,6 +1131,7 @@ struct WgradArgs {
   float* out;  // [E][M][N]
   int32_t* status;
   long long wait_limit;
+  long long rows_cap;  // > 0: offsets are a caller's, clamped to [0, rows_cap] here
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -1092,7 +1173,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
   }
-  for (int i = threadIdx.x; i <= E; i += kThreads) offs[i] = g.offsets[i];
+  if (g.rows_cap > 0) {
+    if (warp == 0) load_segments(g.offsets, E, g.rows_cap, 1, 1, offs, nullptr, g.status, blockIdx.x == 0);
+  } else {
+    for (int i = threadIdx.x; i <= E; i += kThreads) offs[i] = g.offsets[i];
+  }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -1245,7 +1330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                           : make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
                                         __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
         __syncwarp();
-        for (int i = 0; i < nrows; ++i) dst[(size_t)(row0 + i) * g.N + col + lane] = stg[i * kStgStride + lane];
+        if (col + lane < g.N)
+          for (int i = 0; i < nrows; ++i) dst[(size_t)(row0 + i) * g.N + col + lane] = stg[i * kStgStride + lane];
         __syncwarp();
       }
       tc_fence_before();
@@ -1332,7 +1418,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
   }
-  for (int i = threadIdx.x; i <= E; i += kThreads) offs[i] = g.offsets[i];
+  if (g.rows_cap > 0) {
+    if (warp == 0) load_segments(g.offsets, E, g.rows_cap, 1, 1, offs, nullptr, g.status, blockIdx.x == 0);
+  } else {
+    for (int i = threadIdx.x; i <= E; i += kThreads) offs[i] = g.offsets[i];
+  }
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), C::kTmemCols);
   tc_fence_before();
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
@@ -1565,12 +1655,12 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
 // comparisons).
 bool pair_mode_enabled() { return (kernel_options() & MOE_KERNEL_NO_CTA_PAIR) == 0; }
 
-// A operand: [rows, K] bf16 row-major; box = 64 k x 128 rows
-bool make_map_a(CUtensorMap* m, const void* base, int rows, int K) {
+// A operand: [rows, K] bf16 row-major (ld: elements between rows, 0 = K); box = 64 k x 128 rows
+bool make_map_a(CUtensorMap* m, const void* base, int rows, int K, long long ld = 0) {
   auto enc = get_encode_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)K * 2};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : K) * 2};
   cuuint32_t box[2] = {BK, BM};
   cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
@@ -1580,11 +1670,11 @@ bool make_map_a(CUtensorMap* m, const void* base, int rows, int K) {
 
 // A operand in boxes of box_rows rows (box = 64 k x box_rows): 16 for segments of a few rows, 8 for
 // the spread placement of mid-length segments
-bool make_map_a_rows(CUtensorMap* m, const void* base, int rows, int K, int box_rows) {
+bool make_map_a_rows(CUtensorMap* m, const void* base, int rows, int K, int box_rows, long long ld = 0) {
   auto enc = get_encode_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)K * 2};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : K) * 2};
   cuuint32_t box[2] = {BK, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
@@ -1632,11 +1722,11 @@ bool make_map_bk(CUtensorMap* m, const void* base, int E, int N, int K, int box_
 }
 
 // MN-major operand of the weight gradients: [rows, C] bf16 row-major; box = 64 columns x box_rows rows
-bool make_map_rows(CUtensorMap* m, const void* base, int rows, int C, int box_rows) {
+bool make_map_rows(CUtensorMap* m, const void* base, int rows, int C, int box_rows, long long ld = 0) {
   auto enc = get_encode_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)C * 2};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : C) * 2};
   cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
@@ -1729,11 +1819,12 @@ cudaError_t launch_dgrad(const void* A, int rows_cap, const void* W, int E, int 
 }
 
 cudaError_t launch_wgrad(const void* A, const void* B, int rows_cap, int M, int N, const int32_t* offsets, int E,
-                         float* out, int32_t* status, long long wait_limit, int grid, cudaStream_t st) {
+                         float* out, int32_t* status, long long wait_limit, int grid, cudaStream_t st,
+                         bool caller_offsets = false, long long lda = 0, long long ldb = 0) {
   const bool pair = pair_mode_enabled();
   const int box_rows = pair ? WgPairCfg::kStageK : WgCfg::kBK;
   CUtensorMap ma, mb;
-  if (!make_map_rows(&ma, A, rows_cap, M, box_rows) || !make_map_rows(&mb, B, rows_cap, N, box_rows))
+  if (!make_map_rows(&ma, A, rows_cap, M, box_rows, lda) || !make_map_rows(&mb, B, rows_cap, N, box_rows, ldb))
     return cudaErrorInvalidValue;
   WgradArgs g{};
   g.offsets = offsets;
@@ -1743,6 +1834,7 @@ cudaError_t launch_wgrad(const void* A, const void* B, int rows_cap, int M, int 
   g.out = out;
   g.status = status;
   g.wait_limit = wait_limit;
+  g.rows_cap = caller_offsets ? rows_cap : 0;
   if (pair) {
     CUtensorMap md;
     if (!make_map_dw(&md, out, E, M, N)) return cudaErrorInvalidValue;
@@ -1806,6 +1898,60 @@ cudaError_t launch_bwd_gemms_sm100(const BwdGemmArgs& a, cudaStream_t st, int* l
   if (err != cudaSuccess) return err;
   ++*launches;
   return cudaSuccess;
+}
+
+// The plain grouped product (moe_grouped_matmul).  Tiles as for the FFN's GEMMs: CTA pairs where an expert
+// fills a pair tile on average, else single-CTA tiles with the row placement for short segments.
+template <int EPI>
+cudaError_t launch_rows(const GroupedArgs& a, cudaStream_t st) {
+  const int rows = (int)a.rows_cap;
+  // the experts that can hold rows: with fewer rows than experts, each held one at most on average
+  const long long avg = a.rows_cap / a.E;
+  GemmArgs g{};
+  g.offsets = a.offsets;
+  g.E = a.E;
+  g.N = a.N;
+  g.K = a.K;
+  g.bias = reinterpret_cast<const __nv_bfloat16*>(a.bias);
+  g.h_out = reinterpret_cast<__nv_bfloat16*>(a.y);
+  g.y = reinterpret_cast<float*>(a.y);
+  g.rows_cap = a.rows_cap;
+  g.ldo = a.ldy;
+  g.status = a.status;
+  g.wait_limit = wait_limit();
+  const int grid = sm_count();
+  CUtensorMap ma, mb, mas;
+  if (!make_map_a(&ma, a.x, rows, a.K, a.ldx)) return cudaErrorInvalidValue;
+  if (avg >= PairCfg::kTileM && pair_mode_enabled()) {
+    const bool ok = a.transpose_w ? make_map_bk(&mb, a.W, a.E, a.N, a.K, PairCfg::kHalfN) : make_map_b(&mb, a.W, a.E, a.K, a.N);
+    if (!ok) return cudaErrorInvalidValue;
+    return a.transpose_w ? launch_pair<EPI, true>(ma, mb, ma, g, grid, st) : launch_pair<EPI>(ma, mb, ma, g, grid, st);
+  }
+  const bool small = avg < 32, spread = !small && avg < BM;
+  g.a_box_rows = small ? 16 : (spread ? 8 : 0);
+  g.spread_rows = spread ? 1 : 0;
+  if (g.a_box_rows > 0 && !make_map_a_rows(&mas, a.x, rows, a.K, g.a_box_rows, a.ldx)) return cudaErrorInvalidValue;
+  const CUtensorMap* as = g.a_box_rows > 0 ? &mas : nullptr;
+  const int bn = a.N > 128 ? 256 : (a.N > 64 ? 128 : 64);
+  if (a.transpose_w) {
+    if (!make_map_bk(&mb, a.W, a.E, a.N, a.K, bn)) return cudaErrorInvalidValue;
+    if (bn == 256) return launch_one<256, EPI, true>(ma, mb, g, grid, st, as);
+    if (bn == 128) return launch_one<128, EPI, true>(ma, mb, g, grid, st, as);
+    return launch_one<64, EPI, true>(ma, mb, g, grid, st, as);
+  }
+  if (!make_map_b(&mb, a.W, a.E, a.K, a.N)) return cudaErrorInvalidValue;
+  if (bn == 256) return launch_one<256, EPI>(ma, mb, g, grid, st, as);
+  if (bn == 128) return launch_one<128, EPI>(ma, mb, g, grid, st, as);
+  return launch_one<64, EPI>(ma, mb, g, grid, st, as);
+}
+
+cudaError_t launch_grouped_matmul_sm100(const GroupedArgs& a, cudaStream_t st) {
+  return a.bf16_out ? launch_rows<EPI_ROWS_BF16>(a, st) : launch_rows<EPI_ROWS_F32>(a, st);
+}
+
+cudaError_t launch_grouped_wgrad_sm100(const GroupedArgs& a, const void* dy, float* dW, cudaStream_t st) {
+  return launch_wgrad(a.x, dy, (int)a.rows_cap, a.K, a.N, a.offsets, a.E, dW, a.status, wait_limit(), sm_count(), st, true,
+                      a.ldx, a.ldy);
 }
 
 bool ffn_gemm1_on_pairs(int H, int F, long long avg_rows) { return pair_tiles_fit(F, H, avg_rows); }

@@ -125,6 +125,17 @@ std::atomic<int> g_kernel_options{0};
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+int num_sms() {
+  static const int n = [] {  // initialised once, thread-safely, on the first call
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+      v = 148;
+    return v;
+  }();
+  return n;
+}
+
 }  // namespace
 
 namespace moe {
@@ -132,6 +143,7 @@ namespace moe {
 int& launch_count() { return g_launches; }
 int kernel_options() { return g_kernel_options.load(std::memory_order_relaxed); }
 long long wait_limit() { return g_wait_limit.load(); }
+int sm_count() { return num_sms(); }
 
 // One NVTX range per entry-point call ("moe_route", "moe_forward", ...), so that a timeline shows the
 // stages of a layer call around its kernels.
@@ -181,17 +193,6 @@ T* at(void* ws, size_t off) {
 }
 
 moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-int num_sms() {
-  static const int n = [] {  // initialised once, thread-safely, on the first call
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
-      v = 148;
-    return v;
-  }();
-  return n;
-}
 
 // ---------------------------------------------------------------- stage bodies (validated) -------
 ReduceArgs reduce_args(const moe_shape_t* s, const moe_io_t* io, void* ws, int do_losses, int do_dispatch);

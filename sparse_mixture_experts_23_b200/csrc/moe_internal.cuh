@@ -168,6 +168,8 @@ int& launch_count();
 int kernel_options();
 // Bound on device-side waits (moe_set_wait_limit), read at each launch.
 long long wait_limit();
+// Multiprocessors of the current device (looked up once).
+int sm_count();
 // One NVTX range per entry-point call, named after the entry point.
 struct NvtxRange {
   explicit NvtxRange(const char* name);
@@ -319,5 +321,25 @@ cudaError_t launch_combine(const float* y, const int32_t* row_of, const float* t
 cudaError_t launch_timeout_probe(int32_t* status, long long limit, cudaStream_t st);
 // out[i] = act(u[i]), out[n + i] = act'(u[i]) with the tensor-core epilogues' arithmetic
 cudaError_t launch_activation_probe(int act, const float* u, float* out, long long n, cudaStream_t st);
+
+// ---- grouped products as entry points of their own (moe_grouped_matmul, moe_grouped_wgrad) ----
+struct GroupedArgs {
+  const int32_t* offsets;
+  int E;
+  long long rows_cap;
+  int K, N;
+  long long ldx, ldy;  // row pitches in elements
+  int transpose_w;     // W[E,N,K] instead of W[E,K,N]
+  int bf16_out;
+  const void* x;
+  const void* W;
+  const void* bias;  // or null
+  void* y;
+  int32_t* status;  // or null
+};
+// Argument rules of the two calls; fills the sizes of g.
+moe_status_t check_matmul(const moe_matmul_t* m, bool wgrad, GroupedArgs* g);
+cudaError_t launch_grouped_matmul_sm100(const GroupedArgs& a, cudaStream_t st);
+cudaError_t launch_grouped_wgrad_sm100(const GroupedArgs& a, const void* dy, float* dW, cudaStream_t st);
 
 }  // namespace moe

@@ -1,0 +1,205 @@
+"""moe_grouped_matmul and moe_grouped_wgrad against products in fp64, expert by expert.
+
+The bounds are those of oplib: (n + 2) 2^-23 of the summed magnitudes, and the output type's rounding."""
+import pytest
+import torch
+
+import sparse_mixture_experts_23_b200 as moe
+from oplib import SUM_STEP, offsets_of, randn, round_bound, segments, strided, within
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def reference(x, W, counts, bias, trans):
+    ref = torch.zeros((x.shape[0], W.shape[1] if trans else W.shape[2]), dtype=torch.float64, device=x.device)
+    mag = torch.zeros_like(ref)
+    for e, r in segments(counts):
+        w = W[e].double().T if trans else W[e].double()
+        ref[r] = x[r].double() @ w
+        mag[r] = x[r].double().abs() @ w.abs()
+        if bias is not None:
+            ref[r] += bias[e].double()
+            mag[r] += bias[e].double().abs()
+    return ref, mag
+
+
+def check_forward(counts, K, N, dtype, out_dtype, trans, bias, pad=0, spare=0, seed=0):
+    E, n = len(counts), sum(counts)
+    x = randn((n + spare, K), dtype, seed)
+    if spare:
+        x[n:] = float("nan")  # rows behind the last segment must not reach any result
+    W = randn((E, N, K) if trans else (E, K, N), dtype, seed + 1, K ** -0.5)
+    b = randn((E, N), dtype, seed + 2) if bias else None
+    ref, mag = reference(x, W, counts, b, trans)
+    step = 8 if dtype == BF else 4
+    xs = strided(x, step * pad)[0] if pad else x
+    out, buf = strided(torch.full((n + spare, N), 7.0, dtype=out_dtype, device="cuda"), step * pad, 7.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = moe.grouped_matmul(xs, W, offsets_of(counts), bias=b, transpose_w=trans, out=out, status=status)
+    assert moe.moe_get_device_status(status.data_ptr()) == moe.MOE_OK
+    assert y.data_ptr() == out.data_ptr()
+    bound = (K + 2) * SUM_STEP * mag
+    within(y[:n], ref[:n], bound[:n] + round_bound(ref[:n].abs() + bound[:n], out_dtype), f"{counts} {K} {N}")
+    assert (buf[n:] == 7.0).all() and (buf[:, N:] == 7.0).all(), "wrote outside its rows or columns"
+
+
+# short segments (16-row boxes), spread segments, full tiles, pair tiles; widths that end inside every tile
+ROWS = [
+    [1], [0, 1, 0], [5, 0, 31, 16, 17], [33, 64, 0, 100, 127], [128, 129, 130], [300, 1, 255, 0],
+    [256, 257, 258], [1, 0, 900, 128], [511, 513],
+]
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts", ROWS, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("K,N", [(64, 256), (8, 8), (72, 72), (200, 328), (136, 520)])
+def test_bf16(counts, K, N, trans):
+    check_forward(counts, K, N, BF, BF, trans, bias=N != 72)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts", ROWS, ids=lambda c: "-".join(map(str, c)))
+def test_bf16_to_fp32(counts, trans):
+    check_forward(counts, 136, 296, BF, F32, trans, bias=True, seed=3)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts", [[1], [0, 3, 64, 65, 0, 130], [63, 1, 300]], ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("K,N", [(4, 4), (16, 128), (20, 132), (100, 260), (516, 68)])
+def test_fp32(counts, K, N, trans):
+    check_forward(counts, K, N, F32, F32, trans, bias=K != 16)
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("counts", [[3, 0, 9], [40, 90], [700, 0, 400]], ids=lambda c: "-".join(map(str, c)))
+def test_strides_and_spare_rows(counts, dtype, out):
+    """Rows at a pitch, rows behind the last segment (NaN in x, untouched in y), columns past N untouched."""
+    for trans in (False, True):
+        check_forward(counts, 72, 200, dtype, out, trans, bias=True, pad=3, spare=70, seed=11)
+
+
+def test_long_contraction_and_many_experts():
+    check_forward([64] * 5, 14336, 264, BF, BF, False, True)
+    check_forward([2] * 100 + [0] * 100 + [3] * 56, 64, 64, BF, BF, False, True)
+    check_forward([1] + [0] * 254 + [1], 64, 64, BF, F32, True, True)
+    check_forward([300] + [0] * 254 + [1], 64, 64, F32, F32, False, True)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_infinities_stay_in_their_rows(dtype):
+    """A row that holds inf or NaN gives what its own sum gives; the rows beside it are unchanged."""
+    counts = [5, 130]
+    x = randn((135, 64), dtype, 1)
+    W = randn((2, 64, 128), dtype, 2)
+    off = offsets_of(counts)
+    clean = moe.grouped_matmul(x, W, off)
+    x[2, 3], x[70, 1], x[71, 0] = float("inf"), float("nan"), float("-inf")
+    y = moe.grouped_matmul(x, W, off)
+    rows = [2, 70, 71]
+    keep = [r for r in range(135) if r not in rows]
+    assert torch.equal(y[keep], clean[keep])
+    assert torch.equal(y[2], torch.sign(W[0, 3]) * float("inf")) and y[70].isnan().all()
+    assert torch.equal(y[71], torch.sign(W[1, 0]) * float("-inf"))
+
+
+def check_wgrad(counts, K, N, dtype, bias, pad=0, spare=0, seed=0):
+    E, n = len(counts), sum(counts)
+    x, dy = randn((n + spare, K), dtype, seed), randn((n + spare, N), dtype, seed + 1)
+    if spare:
+        x[n:], dy[n:] = float("nan"), float("inf")
+    step = 8 if dtype == BF else 4
+    xs, dys = (strided(x, step * pad)[0], strided(dy, 2 * step * pad)[0]) if pad else (x, dy)
+    dW = torch.full((E, K, N), float("nan"), device="cuda")
+    db = torch.full((E, N), float("nan"), device="cuda") if bias else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = moe.grouped_wgrad(xs, dys, offsets_of(counts), dW=dW, db=db, status=status)
+    assert moe.moe_get_device_status(status.data_ptr()) == moe.MOE_OK
+    assert (got[0] if bias else got).data_ptr() == dW.data_ptr()
+    for e, r in segments(counts):
+        a, d, c = x[r].double(), dy[r].double(), counts[e]
+        within(dW[e], a.T @ d, (c + 2) * SUM_STEP * (a.abs().T @ d.abs()), f"dW[{e}] {counts} {K} {N}")
+        if bias:
+            within(db[e], d.sum(0), (c + 2) * SUM_STEP * d.abs().sum(0), f"db[{e}] {counts}")
+    again = moe.grouped_wgrad(xs, dys, offsets_of(counts), bias_grad=bias)
+    assert torch.equal(again[0] if bias else again, dW) and (not bias or torch.equal(again[1], db))
+
+
+@pytest.mark.parametrize("counts", [[1], [0, 1, 0], [5, 0, 16, 17], [127, 128, 129], [300, 0, 1], [1000]],
+                         ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("K,N", [(64, 256), (8, 8), (72, 40), (264, 328)])
+def test_wgrad_bf16(counts, K, N):
+    check_wgrad(counts, K, N, BF, bias=True)
+
+
+@pytest.mark.parametrize("counts", [[1], [0, 15, 16, 17, 0, 130]], ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("K,N", [(4, 4), (64, 128), (68, 132), (100, 36)])
+def test_wgrad_fp32(counts, K, N):
+    check_wgrad(counts, K, N, F32, bias=True)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_wgrad_strides_and_spare_rows(dtype):
+    check_wgrad([40, 0, 99], 72, 200, dtype, bias=True, pad=2, spare=130)
+    check_wgrad([40, 0, 99], 72, 200, dtype, bias=False, spare=1)
+
+
+def test_wgrad_without_rows_is_zero():
+    for rows in (0, 8):  # an empty batch, and one whose rows belong to nobody
+        x, dy = torch.ones((rows, 64), device="cuda", dtype=BF), torch.ones((rows, 32), device="cuda", dtype=BF)
+        dW, db = moe.grouped_wgrad(x, dy, offsets_of([0, 0]), bias_grad=True)
+        assert dW.shape == (2, 64, 32) and not dW.any() and not db.any()
+    assert moe.grouped_matmul(torch.ones((0, 64), device="cuda", dtype=BF),
+                              torch.ones((2, 64, 32), device="cuda", dtype=BF), offsets_of([0, 0])).shape == (0, 32)
+
+
+def test_single_cta_kernels_agree():
+    """The kernels without CTA pairs, on the shapes that would use pairs."""
+    try:
+        moe.moe_set_kernel_options(moe.MOE_KERNEL_NO_CTA_PAIR)
+        check_forward([300, 0, 513], 136, 520, BF, BF, False, True, pad=1, spare=3)
+        check_forward([300, 0, 513], 136, 520, BF, F32, True, True, pad=1, spare=3)
+        check_wgrad([300, 0, 513], 136, 40, BF, True, pad=1, spare=3)
+    finally:
+        moe.moe_set_kernel_options(0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad", [[0, 5, 3, 9], [1, 5, 7, 9], [0, 5, 7, 1000], [-4, 5, 7, 9], [0, -1, 7, 9]])
+def test_bad_offsets_are_clamped_and_reported(dtype, bad):
+    x, W = randn((9, 64), dtype, 1), randn((3, 64, 64), dtype, 2)
+    off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.grouped_matmul(x, W, off, status=status)
+    assert moe.moe_get_device_status(status.data_ptr()) == moe.MOE_ERR_INVALID_ARG
+    moe.grouped_wgrad(x, x, off, status=status)
+    assert moe.moe_get_device_status(status.data_ptr()) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_get_device_status(status.data_ptr()) == moe.MOE_OK
+
+
+def test_graph_replay_and_side_stream():
+    """Captured once, replayed on new inputs and new offsets; two calls at once on two streams."""
+    counts, other = [30, 0, 70], [1, 98, 1]
+    x, W = randn((100, 64), BF, 1), randn((3, 64, 128), BF, 2)
+    off = offsets_of(counts)
+    y, dW = torch.empty((100, 128), dtype=BF, device="cuda"), torch.empty((3, 64, 128), device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        moe.grouped_matmul(x, W, off, out=y)
+        moe.grouped_wgrad(x, y, off, dW=dW)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.grouped_matmul(x, W, off, out=y)
+        moe.grouped_wgrad(x, y, off, dW=dW)
+    x.copy_(randn((100, 64), BF, 5))
+    off.copy_(offsets_of(other))
+    g.replay()
+    torch.cuda.synchronize()
+    y2 = moe.grouped_matmul(x, W, off)
+    assert torch.equal(y, y2) and torch.equal(dW, moe.grouped_wgrad(x, y2, off))
+    ref, mag = reference(x, W, other, None, False)
+    bound = 66 * SUM_STEP * mag
+    within(y, ref, bound + round_bound(ref.abs() + bound, BF))

@@ -1,0 +1,95 @@
+"""Argument checks of the experts' operators: every refusal comes before any CUDA work, so none needs a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import sparse_mixture_experts_23_b200 as moe
+from sparse_mixture_experts_23_b200 import build as moe_build
+
+FAKE = 1 << 20  # an aligned non-null "device" address; never dereferenced by these calls
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    moe_build.build()
+    return moe.load_library()
+
+
+def matmul(**kw):
+    d = dict(E=4, rows_cap=100, K=64, N=128, dtype=1, out_dtype=1, transpose_w=0, ldx=0, ldy=0)
+    d.update(kw)
+    return moe.Matmul(**d)
+
+
+BAD_SIZES = [
+    (dict(E=0), moe.MOE_ERR_INVALID_ARG), (dict(E=257), moe.MOE_ERR_INVALID_ARG), (dict(rows_cap=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(K=0), moe.MOE_ERR_INVALID_ARG), (dict(N=0), moe.MOE_ERR_INVALID_ARG), (dict(N=-8), moe.MOE_ERR_INVALID_ARG),
+    (dict(dtype=2), moe.MOE_ERR_INVALID_ARG), (dict(ldx=56), moe.MOE_ERR_INVALID_ARG), (dict(ldy=120), moe.MOE_ERR_INVALID_ARG),
+    (dict(K=60), moe.MOE_ERR_UNSUPPORTED), (dict(N=100), moe.MOE_ERR_UNSUPPORTED), (dict(ldx=68), moe.MOE_ERR_UNSUPPORTED),
+    (dict(ldy=132), moe.MOE_ERR_UNSUPPORTED), (dict(dtype=0, out_dtype=0, K=62), moe.MOE_ERR_UNSUPPORTED),
+    (dict(rows_cap=(1 << 31) - 1024), moe.MOE_ERR_UNSUPPORTED), (dict(N=1 << 23), moe.MOE_ERR_UNSUPPORTED),
+    (dict(rows_cap=1 << 30, N=1 << 20), moe.MOE_ERR_UNSUPPORTED), (dict(ldx=1 << 37), moe.MOE_ERR_UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("bad,code", BAD_SIZES)
+def test_matmul_sizes(bad, code):
+    m = matmul(**bad)
+    assert moe.moe_grouped_matmul(m, FAKE, FAKE, FAKE, None, FAKE) == code
+    if "rows_cap" not in bad or bad["rows_cap"] != 1 << 30:  # the weight gradient has no tile per row block
+        assert moe.moe_grouped_wgrad(m, FAKE, FAKE, FAKE, FAKE) == code
+    assert moe.moe_last_launch_count() == 0
+
+
+def test_matmul_types_and_pointers():
+    for bad, code in ((dict(out_dtype=2), moe.MOE_ERR_INVALID_ARG), (dict(dtype=0, out_dtype=1), moe.MOE_ERR_UNSUPPORTED)):
+        assert moe.moe_grouped_matmul(matmul(**bad), FAKE, FAKE, FAKE, None, FAKE) == code
+    ok = [FAKE, FAKE, FAKE, None, FAKE]
+    for i in (0, 1, 2, 4):  # offsets, x, W, y
+        for p in (None, FAKE + 2):
+            args = list(ok)
+            args[i] = p
+            assert moe.moe_grouped_matmul(matmul(), *args) == moe.MOE_ERR_INVALID_ARG, (i, p)
+            assert moe.moe_grouped_wgrad(matmul(), *args[:3], args[4] if i == 4 else FAKE) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_grouped_matmul(matmul(), FAKE, FAKE, FAKE, FAKE + 8, FAKE) == moe.MOE_ERR_INVALID_ARG  # bias
+    assert moe.moe_grouped_matmul(matmul(), FAKE, FAKE, FAKE, None, FAKE, FAKE + 1) == moe.MOE_ERR_INVALID_ARG  # status
+    assert moe.moe_grouped_wgrad(matmul(), FAKE, FAKE, FAKE, FAKE, FAKE + 4) == moe.MOE_ERR_INVALID_ARG  # db
+    lib = moe.load_library()
+    assert lib.moe_grouped_matmul(None, FAKE, FAKE, FAKE, None, FAKE, None, None) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_grouped_matmul(matmul(rows_cap=0), None, None, None, None, None) == moe.MOE_OK
+    assert moe.moe_last_launch_count() == 0
+
+
+def test_matmul_struct_layout():
+    assert ctypes.sizeof(moe.Matmul) == 56 and moe.Matmul.ldx.offset == 40 and moe.Matmul.K.offset == 16
+
+
+BF = torch.bfloat16
+
+
+def z(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype)
+
+
+@pytest.mark.parametrize("call,message", [
+    (lambda: moe.grouped_matmul(z(4, 64, dtype=torch.float16), z(2, 64, 8), z(3, dtype=torch.int32)), "float32 or bfloat16"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 64, 8, dtype=torch.float32), z(3, dtype=torch.int32)), "W must be"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(3, 64, 8), z(3, dtype=torch.int32)), "W must have shape"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 64, 8), z(3, dtype=torch.int64)), "offsets"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 64, 8), z(6, dtype=torch.int32)[::2]), "offsets"),
+    (lambda: moe.grouped_matmul(z(64, 4).T, z(2, 64, 8), z(3, dtype=torch.int32)), "contiguous"),
+    (lambda: moe.grouped_matmul(z(1, 64).expand(4, 64), z(2, 64, 8), z(3, dtype=torch.int32)), "overlap"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 64, 8), z(3, dtype=torch.int32), bias=z(2, 16)), "bias must have shape"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 64, 8), z(3, dtype=torch.int32), out=z(4, 16)), "out must have shape"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 64, 8), z(3, dtype=torch.int32), out=z(4, 8), out_dtype=torch.float32),
+     "another type"),
+    (lambda: moe.grouped_matmul(z(4, 64), z(2, 64, 8), z(3, dtype=torch.int32)), "needs CUDA tensors"),
+    (lambda: moe.grouped_wgrad(z(4, 64), z(5, 8), z(3, dtype=torch.int32)), "same number of rows"),
+    (lambda: moe.grouped_wgrad(z(4, 64), z(4, 8, dtype=torch.float32), z(3, dtype=torch.int32)), "dy must be"),
+    (lambda: moe.grouped_wgrad(z(4, 64), z(4, 8), z(3, dtype=torch.int32), dW=z(2, 64, 8)), "dW must be"),
+    (lambda: moe.grouped_wgrad(z(4, 64), z(4, 8), z(3, dtype=torch.int32)), "needs CUDA tensors"),
+])
+def test_tensor_checks(call, message):
+    with pytest.raises(ValueError, match=message):
+        call()
