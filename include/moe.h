@@ -100,6 +100,8 @@ typedef enum { MOE_ROUTING_TOKEN_CHOICE = 0, MOE_ROUTING_EXPERT_CHOICE = 1 } moe
 /* Activation between the two expert Linear layers.  GELU is the exact erf form (Quick Start
  * expert, nn.GELU()); SiLU is u * sigmoid(u) (Advanced Patterns, Mixtral block experts). */
 typedef enum { MOE_ACT_GELU = 0, MOE_ACT_SILU = 1 } moe_activation_t;
+/* No activation, where an operator outside the layer takes one (a layer's shape does not). */
+#define MOE_ACT_NONE (-1)
 
 /* Problem statement.  capacity_factor = +INFINITY means dropless.  Per-expert capacity is
  * max(ceil(capacity_factor * T * k / E), min_capacity) evaluated in double ("MoE Training" page,
@@ -447,6 +449,38 @@ MOE_API moe_status_t moe_grouped_matmul(const moe_matmul_t* m, const int32_t* of
  * checks and errors as above; rows_cap = 0 writes zeros.  1 launch, 1 more with db. */
 MOE_API moe_status_t moe_grouped_wgrad(const moe_matmul_t* m, const int32_t* offsets, const void* x, const void* dy,
                                        float* dW, float* db, int32_t* status, cudaStream_t stream);
+
+/* The expert's hidden step on its own: activation, optional gate (gated experts), dropout.
+ *   forward   y  = m * act(u) * gate / (1 - p)
+ *   backward  du = m * dy * gate * act'(u) / (1 - p),   dgate = m * dy * act(u) / (1 - p)
+ * With MOE_ACT_NONE and no gate it is plain dropout.  The mask m is not stored: element (r, c) is kept
+ * when word c % 4 of Philox4x32-10 (Salmon et al., SC 2011) at counter words (c / 4, r, offset, offset >> 32)
+ * under key words (seed, seed >> 32) is >= floor(p * 2^32).  rng points to {seed, offset} in device memory, so
+ * a captured graph takes new numbers on every replay; the backward pass is given the same two.  Take another
+ * offset (or seed) for every step and layer.  A dropped element is exactly 0, whatever u, gate or dy hold. */
+typedef struct {
+  int64_t rows_cap;    /* rows of every buffer, < 2^32 */
+  const int32_t* rows; /* device: rows in use, e.g. the offsets' last entry; NULL = rows_cap.  Clamped to
+                          [0, rows_cap]; the rows behind it are not read and not written */
+  int32_t F;           /* columns, 1 .. 2^30, any */
+  moe_dtype_t dtype;   /* storage type of every buffer; arithmetic in fp32, one rounding per result */
+  int32_t activation;  /* MOE_ACT_GELU, MOE_ACT_SILU or MOE_ACT_NONE */
+  double p;            /* probability of a zero, 0 .. 1 */
+  const uint64_t* rng; /* device, 8-byte aligned: {seed, offset}; may be NULL when p = 0 */
+  int64_t ld_in;       /* elements between rows of u and of gate; 0 = F */
+  int64_t ld_y;        /* of y (forward) and dy (backward); 0 = F */
+  int64_t ld_grad;     /* of du and dgate; 0 = F */
+} moe_act_t;
+
+/* gate may be NULL (then dgate must be).  y may be u or gate itself, and du, dgate may be dy, u or gate, with
+ * the same pitch; buffers must not overlap otherwise.  Any alignment that the type has is taken; 16-byte
+ * aligned buffers with widths and pitches that 16 bytes divide run wide.  Errors: MOE_ERR_INVALID_ARG (null
+ * or misaligned pointers, F < 1, rows_cap < 0, unknown type or activation, p outside [0, 1] or NaN, p > 0
+ * without rng, a pitch below F), MOE_ERR_UNSUPPORTED (rows_cap or F too large), MOE_ERR_CUDA.
+ * No workspace, no state: any number of calls at once.  1 launch; none for rows_cap = 0. */
+MOE_API moe_status_t moe_act_dropout(const moe_act_t* m, const void* u, const void* gate, void* y, cudaStream_t stream);
+MOE_API moe_status_t moe_act_dropout_backward(const moe_act_t* m, const void* dy, const void* u, const void* gate,
+                                              void* du, void* dgate, cudaStream_t stream);
 
 /* Kernel-selection switches for side-by-side comparisons of the kernels; normal use needs none.
  *   MOE_KERNEL_NO_CTA_PAIR  single-CTA 128-row grouped-GEMM tiles everywhere, instead of the CTA-pair

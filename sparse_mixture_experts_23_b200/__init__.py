@@ -20,6 +20,7 @@ MOE_DTYPE_F32, MOE_DTYPE_BF16 = 0, 1
 DTYPES = {"f32": MOE_DTYPE_F32, "bf16": MOE_DTYPE_BF16}
 MOE_ACT_GELU, MOE_ACT_SILU = 0, 1
 ACTIVATIONS = {"gelu": MOE_ACT_GELU, "silu": MOE_ACT_SILU}
+MOE_ACT_NONE = -1  # for the operators outside the layer
 MOE_ROUTING_TOKEN_CHOICE, MOE_ROUTING_EXPERT_CHOICE = 0, 1
 ROUTINGS = {"token_choice": MOE_ROUTING_TOKEN_CHOICE, "expert_choice": MOE_ROUTING_EXPERT_CHOICE}
 
@@ -30,6 +31,7 @@ ENTRY_POINTS = (
     "moe_train_workspace_size", "moe_forward_train", "moe_backward", "moe_loss_sums", "moe_losses_from_sums",
     "moe_set_kernel_options", "moe_get_kernel_options", "moe_copy_row_segments", "moe_expert_ffn_rows",
     "moe_expert_ffn_rows_workspace_size", "moe_debug_activation", "moe_grouped_matmul", "moe_grouped_wgrad",
+    "moe_act_dropout", "moe_act_dropout_backward",
 )
 MOE_KERNEL_DEFAULT, MOE_KERNEL_NO_CTA_PAIR, MOE_KERNEL_NO_TC_GATE, MOE_KERNEL_NO_TMA_ROUTER = 0, 1, 2, 4
 
@@ -67,6 +69,13 @@ class Matmul(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int32), ("rows_cap", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("transpose_w", ctypes.c_int32),
                 ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class Act(ctypes.Structure):
+    """moe_act_t: the hidden step's sizes, activation, dropout and row pitches."""
+    _fields_ = [("rows_cap", ctypes.c_int64), ("rows", ctypes.c_void_p), ("F", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("activation", ctypes.c_int32), ("p", ctypes.c_double), ("rng", ctypes.c_void_p),
+                ("ld_in", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("ld_grad", ctypes.c_int64)]
 
 
 class RowSegment(ctypes.Structure):
@@ -130,6 +139,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_grouped_matmul.restype = st
     lib.moe_grouped_wgrad.argtypes = [P(Matmul), vp, vp, vp, vp, vp, vp, vp]
     lib.moe_grouped_wgrad.restype = st
+    lib.moe_act_dropout.argtypes = [P(Act), vp, vp, vp, vp]
+    lib.moe_act_dropout.restype = st
+    lib.moe_act_dropout_backward.argtypes = [P(Act), vp, vp, vp, vp, vp, vp]
+    lib.moe_act_dropout_backward.restype = st
     lib.moe_debug_activation.argtypes = [ctypes.c_int, vp, vp, ctypes.c_int64, vp]
     lib.moe_debug_activation.restype = st
     lib.moe_debug_timeout_probe.argtypes = [vp, sz, vp]
@@ -287,6 +300,14 @@ def moe_grouped_wgrad(m: Matmul, offsets, x, dy, dW, db=None, status=None, strea
     return load_library().moe_grouped_wgrad(ctypes.byref(m), offsets, x, dy, dW, db, status, stream)
 
 
+def moe_act_dropout(m: Act, u, gate, y, stream=0) -> int:
+    return load_library().moe_act_dropout(ctypes.byref(m), u, gate, y, stream)
+
+
+def moe_act_dropout_backward(m: Act, dy, u, gate, du, dgate=None, stream=0) -> int:
+    return load_library().moe_act_dropout_backward(ctypes.byref(m), dy, u, gate, du, dgate, stream)
+
+
 def moe_debug_activation(activation: int, u, out, n: int, stream=0) -> int:
     return load_library().moe_debug_activation(int(activation), u, out, int(n), stream)
 
@@ -430,7 +451,7 @@ class MoEBuffers:
 
 
 # The operators on torch tensors, imported on first use: the binding itself loads without torch.
-_OPERATORS = ("grouped_matmul", "grouped_wgrad")
+_OPERATORS = ("grouped_matmul", "grouped_wgrad", "act_dropout", "act_dropout_backward")
 
 
 def __getattr__(name):

@@ -1,0 +1,259 @@
+// The expert's hidden step in training: activation, optional gate, dropout.
+//   forward   y = m act(u) g / (1 - p)
+//   backward  dg = m dy act(u) / (1 - p),  du = m dy g act'(u) / (1 - p)
+// ("MoE Training: Mixture of Experts" page, Quick Start: the activation between the expert's two Linear
+// layers.)  g is 1 without a gate.  The mask m is never stored: element (row r, column c) keeps its value
+// when word c % 4 of Philox4x32-10 (J. Salmon et al., Parallel random numbers: as easy as 1, 2, 3, SC 2011)
+// at counter (c / 4, r, offset, offset >> 32) under key (seed, seed >> 32) is at least p 2^32, and the
+// backward pass computes the same words again.  A dropped element is 0 whatever its inputs hold.
+//
+// Bound: HBM.  One vector of 16 bytes (8 bf16 or 4 fp32 columns: whole Philox blocks) of one row per thread
+// and step, two rows in flight; ten Philox rounds are 20 wide multiplies for four elements, less than the
+// time that an SM waits for their bytes.  All arithmetic is fp32; each output is rounded once.
+#include <cuda_bf16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "activation.cuh"
+#include "moe_internal.cuh"
+
+namespace moe {
+namespace {
+
+struct ActArgs {
+  const void* dy;
+  const void* u;
+  const void* gate;  // or null
+  void* y;           // forward: y; backward: du
+  void* dgate;
+  const int32_t* rows;  // device count, or null
+  const unsigned long long* rng;
+  long long rows_cap, ld_in, ld_y, ld_grad;
+  int F;
+  unsigned thr;  // keep when word >= thr (thr_all: none)
+  int drop, drop_all;
+  float scale;
+};
+
+__device__ __forceinline__ void philox4x32_10(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t p0 = (uint64_t)0xD2511F53u * c[0], p1 = (uint64_t)0xCD9E8D57u * c[2];
+    c[0] = (uint32_t)(p1 >> 32) ^ c[1] ^ k0;
+    c[1] = (uint32_t)p1;
+    c[2] = (uint32_t)(p0 >> 32) ^ c[3] ^ k1;
+    c[3] = (uint32_t)p0;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+
+// V columns of one row: with VEC one 16-byte access, otherwise element by element up to n columns (rows or
+// widths that 16 bytes do not divide)
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ void load_cols(const T* p, int n, float (&v)[V]) {
+  if constexpr (VEC) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 2) {
+        v[2 * j] = __uint_as_float(a[j] << 16);
+        v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
+      } else {
+        v[j] = __uint_as_float(a[j]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = j < n ? (float)p[j] : 0.f;
+  }
+}
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ void store_cols(T* p, int n, const float (&v)[V]) {
+  if constexpr (VEC) {
+    uint32_t a[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        a[j] = *reinterpret_cast<const uint32_t*>(&b);
+      } else {
+        a[j] = __float_as_uint(v[j]);
+      }
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(a[0], a[1], a[2], a[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < n) p[j] = (T)v[j];
+  }
+}
+
+template <typename T, int ACT, bool BWD, bool GATE, bool VEC>
+__global__ void __launch_bounds__(256) act_dropout_kernel(ActArgs a) {
+  constexpr int V = 16 / sizeof(T);
+  constexpr bool FAST = sizeof(T) == 2;
+  constexpr int U = 2;  // rows in flight
+  const int col = (blockIdx.x * blockDim.x + threadIdx.x) * V;
+  if (col >= a.F) return;
+  const int n = a.F - col;
+  long long rows = a.rows_cap;
+  if (a.rows != nullptr) {
+    const int r = *a.rows;
+    rows = r < 0 ? 0 : (r < rows ? r : rows);
+  }
+  uint32_t key[2] = {}, off[2] = {};
+  if (a.drop) {
+    const unsigned long long seed = a.rng[0], o = a.rng[1];
+    key[0] = (uint32_t)seed;
+    key[1] = (uint32_t)(seed >> 32);
+    off[0] = (uint32_t)o;
+    off[1] = (uint32_t)(o >> 32);
+  }
+  const long long step = (long long)gridDim.y * blockDim.y;
+  for (long long r0 = (long long)blockIdx.y * blockDim.y + threadIdx.y; r0 < rows; r0 += U * step) {
+    float u[U][V], g[U][V], d[U][V];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const long long r = r0 + q * step;
+      if (r >= rows) break;
+      load_cols<T, V, VEC>(static_cast<const T*>(a.u) + r * a.ld_in + col, n, u[q]);
+      if constexpr (GATE) load_cols<T, V, VEC>(static_cast<const T*>(a.gate) + r * a.ld_in + col, n, g[q]);
+      if constexpr (BWD) load_cols<T, V, VEC>(static_cast<const T*>(a.dy) + r * a.ld_y + col, n, d[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const long long r = r0 + q * step;
+      if (r >= rows) break;
+      uint32_t w[V];
+      if (a.drop) {
+#pragma unroll
+        for (int b = 0; b < V / 4; ++b) {
+          uint32_t c[4] = {(uint32_t)(col / 4 + b), (uint32_t)r, off[0], off[1]};
+          philox4x32_10(c, key[0], key[1]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[4 * b + j] = c[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const bool keep = !a.drop_all && (!a.drop || w[j] >= a.thr);
+        if constexpr (BWD) {
+          float da;
+          const float act = activate_grad<ACT, FAST>(u[q][j], da);
+          const float dm = a.scale * d[q][j];
+          u[q][j] = keep ? (GATE ? dm * g[q][j] * da : dm * da) : 0.f;
+          if constexpr (GATE) g[q][j] = keep ? dm * act : 0.f;
+        } else {
+          const float v = a.scale * activate<ACT, FAST>(u[q][j]);
+          u[q][j] = keep ? (GATE ? v * g[q][j] : v) : 0.f;
+        }
+      }
+      if constexpr (BWD) {
+        store_cols<T, V, VEC>(static_cast<T*>(a.y) + r * a.ld_grad + col, n, u[q]);
+        if constexpr (GATE) store_cols<T, V, VEC>(static_cast<T*>(a.dgate) + r * a.ld_grad + col, n, g[q]);
+      } else {
+        store_cols<T, V, VEC>(static_cast<T*>(a.y) + r * a.ld_y + col, n, u[q]);
+      }
+    }
+  }
+}
+
+template <typename T, int ACT, bool BWD, bool GATE, bool VEC>
+cudaError_t launch_act(const ActArgs& a, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const int vecs = (a.F + V - 1) / V;
+  int bx = 32;  // threads across a row: a power of two up to the block, so narrow rows share one
+  while (bx < 256 && bx < vecs) bx *= 2;
+  const int by = 256 / bx;
+  const long long gx = (vecs + bx - 1) / bx;
+  // two rows a thread where there are rows enough for every SM's 8 blocks
+  long long gy = (a.rows_cap + 2 * by - 1) / (2 * by);
+  if (gx * gy < 8LL * sm_count()) gy = (a.rows_cap + by - 1) / by;
+  if (gy > 65535) gy = 65535;
+  act_dropout_kernel<T, ACT, BWD, GATE, VEC><<<dim3((unsigned)gx, (unsigned)gy), dim3(bx, by), 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int ACT, bool BWD>
+cudaError_t launch_by_form(const ActArgs& a, bool vec, cudaStream_t st) {
+  if (a.gate != nullptr) return vec ? launch_act<T, ACT, BWD, true, true>(a, st) : launch_act<T, ACT, BWD, true, false>(a, st);
+  return vec ? launch_act<T, ACT, BWD, false, true>(a, st) : launch_act<T, ACT, BWD, false, false>(a, st);
+}
+
+template <bool BWD>
+cudaError_t launch_by_type(const ActArgs& a, int dtype, int act, bool vec, cudaStream_t st) {
+  if (dtype == MOE_DTYPE_BF16) {
+    if (act == MOE_ACT_GELU) return launch_by_form<__nv_bfloat16, MOE_ACT_GELU, BWD>(a, vec, st);
+    if (act == MOE_ACT_SILU) return launch_by_form<__nv_bfloat16, MOE_ACT_SILU, BWD>(a, vec, st);
+    return launch_by_form<__nv_bfloat16, MOE_ACT_NONE, BWD>(a, vec, st);
+  }
+  if (act == MOE_ACT_GELU) return launch_by_form<float, MOE_ACT_GELU, BWD>(a, vec, st);
+  if (act == MOE_ACT_SILU) return launch_by_form<float, MOE_ACT_SILU, BWD>(a, vec, st);
+  return launch_by_form<float, MOE_ACT_NONE, BWD>(a, vec, st);
+}
+
+moe_status_t run_act(const moe_act_t* m, const void* dy, const void* u, const void* gate, void* y, void* dgate, bool bwd,
+                     cudaStream_t st) {
+  int& launches = launch_count();
+  launches = 0;
+  if (m == nullptr || m->rows_cap < 0 || m->F < 1) return MOE_ERR_INVALID_ARG;
+  if (m->dtype != MOE_DTYPE_F32 && m->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (m->activation != MOE_ACT_GELU && m->activation != MOE_ACT_SILU && m->activation != MOE_ACT_NONE)
+    return MOE_ERR_INVALID_ARG;
+  if (!(m->p >= 0.0 && m->p <= 1.0) || (m->p > 0.0 && m->rng == nullptr)) return MOE_ERR_INVALID_ARG;
+  ActArgs a{};
+  a.ld_in = m->ld_in == 0 ? m->F : m->ld_in;
+  a.ld_y = m->ld_y == 0 ? m->F : m->ld_y;
+  a.ld_grad = m->ld_grad == 0 ? m->F : m->ld_grad;
+  if (a.ld_in < m->F || a.ld_y < m->F || a.ld_grad < m->F) return MOE_ERR_INVALID_ARG;
+  const uintptr_t es = m->dtype == MOE_DTYPE_BF16 ? 2 : 4;
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(u) | reinterpret_cast<uintptr_t>(gate) |
+                         reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(dgate);
+  if (bits % es != 0 || reinterpret_cast<uintptr_t>(m->rng) % 8 != 0 || reinterpret_cast<uintptr_t>(m->rows) % 4 != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (m->rows_cap >= (1LL << 32) || m->F > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  if (m->rows_cap == 0) return MOE_OK;
+  if (u == nullptr || y == nullptr || (bwd && (dy == nullptr || (gate != nullptr) != (dgate != nullptr))))
+    return MOE_ERR_INVALID_ARG;
+  a.dy = dy;
+  a.u = u;
+  a.gate = gate;
+  a.y = y;
+  a.dgate = dgate;
+  a.rows = m->rows;
+  a.rng = reinterpret_cast<const unsigned long long*>(m->rng);
+  a.rows_cap = m->rows_cap;
+  a.F = m->F;
+  const double t = floor(m->p * 4294967296.0);
+  a.drop_all = t >= 4294967296.0;
+  a.thr = a.drop_all ? 0u : (unsigned)t;
+  a.drop = !a.drop_all && a.thr > 0u;
+  a.scale = a.drop_all ? 0.f : (float)(1.0 / (1.0 - m->p));
+  const int v = 16 / (int)es;
+  const bool vec = bits % 16 == 0 && m->F % v == 0 && a.ld_in % v == 0 && a.ld_y % v == 0 && a.ld_grad % v == 0;
+  const cudaError_t err = bwd ? launch_by_type<true>(a, m->dtype, m->activation, vec, st)
+                              : launch_by_type<false>(a, m->dtype, m->activation, vec, st);
+  if (err != cudaSuccess) return MOE_ERR_CUDA;
+  ++launches;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+moe_status_t moe_act_dropout(const moe_act_t* m, const void* u, const void* gate, void* y, cudaStream_t stream) {
+  moe::NvtxRange nvtx_range("moe_act_dropout");
+  return moe::run_act(m, nullptr, u, gate, y, nullptr, false, stream);
+}
+
+moe_status_t moe_act_dropout_backward(const moe_act_t* m, const void* dy, const void* u, const void* gate, void* du,
+                                      void* dgate, cudaStream_t stream) {
+  moe::NvtxRange nvtx_range("moe_act_dropout_backward");
+  return moe::run_act(m, dy, u, gate, du, dgate, true, stream);
+}
+
+}  // extern "C"

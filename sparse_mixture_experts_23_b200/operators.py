@@ -1,4 +1,5 @@
-"""The experts' operators on torch tensors: matrix products grouped by expert and their gradients.
+"""The experts' operators on torch tensors: matrix products grouped by expert, the activation with gate and
+dropout between them, and their gradients.
 
 Like ``MoEBuffers`` these functions only marshal arguments: they check shapes, types and devices, allocate
 what the caller did not pass, and call the C entry point of the same meaning (``moe_grouped_matmul`` ...) on
@@ -127,3 +128,70 @@ def grouped_wgrad(x, dy, offsets, bias_grad: bool = False, dW=None, db=None, sta
           dy.data_ptr(), _dense(dW, "dW", device, torch.float32, (E, K, N)),
           _dense(db, "db", device, torch.float32, (E, N)), _status(status, device))
     return dW if db is None else (dW, db)
+
+
+def _activation(name) -> int:
+    if name is None:
+        return _moe.MOE_ACT_NONE
+    _need(name in _moe.ACTIVATIONS, f"unknown activation {name!r}")
+    return _moe.ACTIVATIONS[name]
+
+
+def _like(t, name: str, like, ld=None) -> int:
+    """t has like's shape and type; with ld, also that row pitch."""
+    _need(t.dtype == like.dtype, f"{name} must be {like.dtype}, not {t.dtype}")
+    _need(t.shape == like.shape, f"{name} must have shape {tuple(like.shape)}, not {tuple(t.shape)}")
+    got = _rows(t, name, like.device)
+    _need(ld is None or like.shape[0] <= 1 or got == ld, f"the rows of {name} must be {ld} elements apart, not {got}")
+    return got
+
+
+def _act(u, gate, activation, p, rng, rows):
+    device = u.device
+    code = _dtype(u, "u")
+    ld = _rows(u, "u", device)
+    if gate is not None:
+        _like(gate, "gate", u, ld)
+    if rng is not None:
+        _need(rng.device == device and rng.dtype in (torch.int64, torch.uint64) and rng.numel() == 2 and rng.is_contiguous(),
+              "rng must hold two 64-bit integers (seed, offset) on u's device")
+    if rows is not None:
+        _need(rows.device == device and rows.dtype == torch.int32 and rows.numel() == 1,
+              "rows must be one int32 on u's device")
+    return _moe.Act(u.shape[0], None if rows is None else rows.data_ptr(), u.shape[1], code, _activation(activation), p,
+                    None if rng is None else rng.data_ptr(), ld, 0, 0)
+
+
+def act_dropout(u, gate=None, activation="gelu", p: float = 0.0, rng=None, rows=None, out=None):
+    """``act(u) * gate``, with each element zeroed with probability p and the others scaled by ``1 / (1 - p)``.
+
+    u and gate ``[rows, F]`` (bf16 or f32; rows may be strided, both by the same pitch, so they can be the two
+    halves of one product's columns), activation "gelu", "silu" or None (plain dropout), rng two int64 on the
+    device: seed and offset of the generator, of which the backward pass wants the same.  ``rows``: an int32
+    on the device (``offsets[-1:]``), the rows in use; those behind it are left as they are in ``out``, which
+    may be u or gate."""
+    m = _act(u, gate, activation, p, rng, rows)
+    if out is None:
+        out = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+    m.ld_y = _like(out, "out", u)
+    _call("moe_act_dropout", u.device, _moe.load_library().moe_act_dropout, ctypes.byref(m), u.data_ptr(),
+          None if gate is None else gate.data_ptr(), out.data_ptr())
+    return out
+
+
+def act_dropout_backward(dy, u, gate=None, activation="gelu", p: float = 0.0, rng=None, rows=None, du=None, dgate=None):
+    """Gradients of ``act_dropout`` for the same u, gate, activation, p and rng: du, or (du, dgate) with a gate.
+    du and dgate may be strided (by the same pitch) and may be dy, u or gate."""
+    m = _act(u, gate, activation, p, rng, rows)
+    m.ld_y = _like(dy, "dy", u)
+    if du is None:
+        du = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+    m.ld_grad = _like(du, "du", u)
+    _need(gate is not None or dgate is None, "dgate without a gate")
+    if gate is not None:
+        if dgate is None:
+            dgate = torch.empty_strided(du.shape, du.stride(), dtype=u.dtype, device=u.device)
+        _like(dgate, "dgate", u, m.ld_grad)
+    _call("moe_act_dropout_backward", u.device, _moe.load_library().moe_act_dropout_backward, ctypes.byref(m), dy.data_ptr(),
+          u.data_ptr(), None if gate is None else gate.data_ptr(), du.data_ptr(), None if dgate is None else dgate.data_ptr())
+    return du if gate is None else (du, dgate)

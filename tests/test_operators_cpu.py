@@ -93,3 +93,67 @@ def z(*shape, dtype=BF):
 def test_tensor_checks(call, message):
     with pytest.raises(ValueError, match=message):
         call()
+
+
+# ---------------------------------------------------------------- activation with dropout
+def act(**kw):
+    d = dict(rows_cap=10, rows=None, F=64, dtype=1, activation=0, p=0.5, rng=FAKE, ld_in=0, ld_y=0, ld_grad=0)
+    d.update(kw)
+    return moe.Act(**d)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(rows_cap=-1), moe.MOE_ERR_INVALID_ARG), (dict(F=0), moe.MOE_ERR_INVALID_ARG), (dict(dtype=2), moe.MOE_ERR_INVALID_ARG),
+    (dict(activation=2), moe.MOE_ERR_INVALID_ARG), (dict(activation=-2), moe.MOE_ERR_INVALID_ARG),
+    (dict(p=-0.1), moe.MOE_ERR_INVALID_ARG), (dict(p=1.5), moe.MOE_ERR_INVALID_ARG), (dict(p=float("nan")), moe.MOE_ERR_INVALID_ARG),
+    (dict(rng=None), moe.MOE_ERR_INVALID_ARG), (dict(rng=FAKE + 4), moe.MOE_ERR_INVALID_ARG), (dict(rows=FAKE + 2), moe.MOE_ERR_INVALID_ARG),
+    (dict(ld_in=63), moe.MOE_ERR_INVALID_ARG), (dict(ld_y=8), moe.MOE_ERR_INVALID_ARG), (dict(ld_grad=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(rows_cap=1 << 32), moe.MOE_ERR_UNSUPPORTED), (dict(F=(1 << 30) + 1), moe.MOE_ERR_UNSUPPORTED),
+])
+def test_act_sizes(bad, code):
+    m = act(**bad)
+    assert moe.moe_act_dropout(m, FAKE, None, FAKE) == code
+    assert moe.moe_act_dropout_backward(m, FAKE, FAKE, None, FAKE) == code
+    assert moe.moe_last_launch_count() == 0
+
+
+def test_act_pointers():
+    assert moe.moe_act_dropout(act(), None, None, FAKE) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_act_dropout(act(), FAKE, None, None) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_act_dropout(act(), FAKE + 1, None, FAKE) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_act_dropout(act(dtype=0), FAKE, FAKE + 2, FAKE) == moe.MOE_ERR_INVALID_ARG
+    for args in ((None, FAKE, None, FAKE, None), (FAKE, FAKE, FAKE, FAKE, None), (FAKE, FAKE, None, FAKE, FAKE)):
+        assert moe.moe_act_dropout_backward(act(), *args) == moe.MOE_ERR_INVALID_ARG
+    assert moe.load_library().moe_act_dropout(None, FAKE, None, FAKE, None) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_act_dropout(act(rows_cap=0), None, None, None) == moe.MOE_OK
+    assert ctypes.sizeof(moe.Act) == 72 and moe.Act.p.offset == 32
+
+
+def test_philox_known_answers():
+    """The published known-answer vectors of Philox4x32-10, for the generator that the GPU tests compare with."""
+    from philox import philox
+
+    for ctr, key, want in (
+            ([0] * 4, [0] * 2, "6627e8d5 e169c58d bc57ac4c 9b00dbd8"),
+            ([0xFFFFFFFF] * 4, [0xFFFFFFFF] * 2, "408f276d 41c83b0e a20bc7c6 6d5451fd"),
+            ([0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344], [0xA4093822, 0x299F31D0],
+             "d16cfe09 94fdcceb 5001e420 24126ea1")):
+        assert " ".join(f"{int(v):08x}" for v in philox(ctr, key)) == want
+
+
+@pytest.mark.parametrize("call,message", [
+    (lambda: moe.act_dropout(z(4, 8), activation="relu"), "unknown activation"),
+    (lambda: moe.act_dropout(z(4, 8), gate=z(4, 9)), "gate must have shape"),
+    (lambda: moe.act_dropout(z(4, 8), gate=z(4, 8, dtype=torch.float32)), "gate must be"),
+    (lambda: moe.act_dropout(z(4, 8), gate=z(4, 16)[:, :8]), "rows of gate"),
+    (lambda: moe.act_dropout(z(4, 8), rng=z(2)), "rng"),
+    (lambda: moe.act_dropout(z(4, 8), rows=z(2, dtype=torch.int32)), "rows must be"),
+    (lambda: moe.act_dropout(z(4, 8), out=z(4, 9)), "out must have shape"),
+    (lambda: moe.act_dropout_backward(z(4, 9), z(4, 8)), "dy must have shape"),
+    (lambda: moe.act_dropout_backward(z(4, 8), z(4, 8), dgate=z(4, 8)), "dgate without"),
+    (lambda: moe.act_dropout_backward(z(4, 8), z(4, 8), gate=z(4, 8), du=z(4, 8), dgate=z(4, 16)[:, :8]), "rows of dgate"),
+    (lambda: moe.act_dropout(z(4, 8)), "needs CUDA tensors"),
+])
+def test_act_tensor_checks(call, message):
+    with pytest.raises(ValueError, match=message):
+        call()
