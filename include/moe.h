@@ -482,6 +482,69 @@ MOE_API moe_status_t moe_act_dropout(const moe_act_t* m, const void* u, const vo
 MOE_API moe_status_t moe_act_dropout_backward(const moe_act_t* m, const void* dy, const void* u, const void* gate,
                                               void* du, void* dgate, cudaStream_t stream);
 
+/* ---- experts in 4 bits (serving) ---------------------------------------------------------------------
+ * Decode reads every weight of the chosen experts for a few rows; held in 4 bits they are a quarter of the
+ * bytes.  A weight W[e,k,n] is s[e,k/G,n] * (c[e,n,k] - 8): codes c in 0..15, two a byte along k (the even k in
+ * the low half), and a bf16 scale for every group of G = 32, 64 or 128 inputs of a column.  The products take
+ * them in a layout of their own, which moe_q4_pack makes once. */
+
+/* Bytes of E experts' packed weights (a device buffer, 16-byte aligned); 0 for sizes that the calls refuse. */
+MOE_API size_t moe_q4_packed_size(int32_t E, int32_t K, int32_t N, int32_t group);
+
+/* codes[E,N,K/2] (uint8) and scales[E,K/group,N] (bf16) from W[E,K,N]: scale = bf16(max |w| / 7) over the group,
+ * code = 8 + round_half_even(w / scale) within 0..15.  A group whose scale rounds to zero gets codes 8; one that
+ * holds an infinity or NaN gets a NaN scale, so that it reads back as NaN.  1 launch. */
+MOE_API moe_status_t moe_q4_quantize(int32_t E, int32_t K, int32_t N, int32_t group, moe_dtype_t dtype, const void* W,
+                                     void* codes, void* scales, cudaStream_t stream);
+/* The packed layout from codes and scales (made above or elsewhere).  1 launch. */
+MOE_API moe_status_t moe_q4_pack(int32_t E, int32_t K, int32_t N, int32_t group, const void* codes, const void* scales,
+                                 void* packed, cudaStream_t stream);
+/* W[E,K,N] = scale * (code - 8) from the packed layout, rounded once to dtype.  1 launch.
+ * Errors of the three: MOE_ERR_INVALID_ARG (E outside [1, 256], K or N < 1, group not 32, 64 or 128, an unknown
+ * dtype, null pointers, codes or packed not 16-byte aligned, others below their type's alignment),
+ * MOE_ERR_UNSUPPORTED (K not a multiple of group, K or N above 2^24, more than 2^31 blocks), MOE_ERR_CUDA. */
+MOE_API moe_status_t moe_q4_dequantize(int32_t E, int32_t K, int32_t N, int32_t group, const void* packed,
+                                       moe_dtype_t dtype, void* W, cudaStream_t stream);
+
+typedef struct {
+  int32_t E;             /* experts, 1..256 */
+  int64_t rows_cap;      /* rows that x and y hold, >= offsets[E]; < 2^31 - 1024 */
+  int32_t K;             /* inputs, a multiple of group */
+  int32_t N;             /* outputs, any */
+  int32_t group;         /* 32, 64 or 128 */
+  moe_dtype_t dtype;     /* type of x and bias */
+  moe_dtype_t out_dtype; /* type of y: either for bf16 x, fp32 for fp32 x; sums are fp32, rounded once at the end */
+  int32_t activation;    /* MOE_ACT_GELU, MOE_ACT_SILU or MOE_ACT_NONE, after the bias */
+  int64_t ldx;           /* elements between rows of x; 0 = K; a multiple of 8 (bf16) or 4 (fp32) */
+  int64_t ldy;           /* elements between rows of y; 0 = N */
+} moe_q4_t;
+
+/* y[r,n] = act(sum_k x[r,k] * W[e,k,n] + bias[e,n]) for every row r of expert e, W in the packed layout.  Rows,
+ * offsets (clamped on the device, and recorded) and what is left unwritten are as in moe_grouped_matmul.
+ * ws: a device buffer of moe_q4_workspace_size() bytes, 256-byte aligned, zero before its first use; calls on
+ * one workspace have to follow each other (one stream, or events between), also as graphs that captured it;
+ * calls on workspaces of their own may run at once.  Its first word is the error word for moe_get_device_status;
+ * after a timeout there, zero the workspace again.  Sums run in a fixed order: the same call gives the same bits
+ * on the same GPU.  Any number of rows is computed; the kernel is made for a few (up to 32 an expert read the
+ * weights once).  Errors: MOE_ERR_INVALID_ARG (sizes and pointers as above; rows_cap < 0; a pitch below the row;
+ * an unknown type or activation; x not 16-byte aligned, y, bias and offsets below their type's alignment; ws null
+ * or misaligned), MOE_ERR_UNSUPPORTED (K not a multiple of group, ldx as above, fp32 x with a bf16 y, K or N above
+ * 2^24, a pitch of 2^31 or more, rows_cap >= 2^31 - 1024), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.
+ * 1 launch; none for rows_cap = 0. */
+MOE_API size_t moe_q4_workspace_size(void);
+MOE_API moe_status_t moe_q4_matmul(const moe_q4_t* m, const int32_t* offsets, const void* x, const void* packed,
+                                   const void* bias, void* y, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The layer's expert FFN with both weights in 4 bits: as moe_expert_ffn between moe_permute and the layer's end,
+ * reading W1q (K = H, N = F) and W2q (K = F, N = H) in place of io->W1 and io->W2 (which may be null).  h is kept
+ * in the storage type and y in fp32, in the layer's workspace; combine = 1 also runs moe_combine's sum into
+ * io->out, 0 leaves y for a later moe_combine.  shape, io, ws and their errors as moe_expert_ffn; group must divide
+ * H and F (MOE_ERR_UNSUPPORTED).  q4_ws: as ws of moe_q4_matmul; errors on the device are recorded in ws.
+ * 2 launches, 3 with combine. */
+MOE_API moe_status_t moe_expert_ffn_q4(const moe_shape_t* shape, const moe_io_t* io, int32_t group, const void* W1q,
+                                       const void* W2q, void* ws, size_t ws_bytes, void* q4_ws, size_t q4_ws_bytes,
+                                       int combine, cudaStream_t stream);
+
 /* Kernel-selection switches for side-by-side comparisons of the kernels; normal use needs none.
  *   MOE_KERNEL_NO_CTA_PAIR  single-CTA 128-row grouped-GEMM tiles everywhere, instead of the CTA-pair
  *                           256 x 256 tiles the long-segment shapes use (forward and backward GEMMs)

@@ -31,7 +31,8 @@ ENTRY_POINTS = (
     "moe_train_workspace_size", "moe_forward_train", "moe_backward", "moe_loss_sums", "moe_losses_from_sums",
     "moe_set_kernel_options", "moe_get_kernel_options", "moe_copy_row_segments", "moe_expert_ffn_rows",
     "moe_expert_ffn_rows_workspace_size", "moe_debug_activation", "moe_grouped_matmul", "moe_grouped_wgrad",
-    "moe_act_dropout", "moe_act_dropout_backward",
+    "moe_act_dropout", "moe_act_dropout_backward", "moe_q4_packed_size", "moe_q4_quantize", "moe_q4_pack",
+    "moe_q4_dequantize", "moe_q4_workspace_size", "moe_q4_matmul", "moe_expert_ffn_q4",
 )
 MOE_KERNEL_DEFAULT, MOE_KERNEL_NO_CTA_PAIR, MOE_KERNEL_NO_TC_GATE, MOE_KERNEL_NO_TMA_ROUTER = 0, 1, 2, 4
 
@@ -76,6 +77,13 @@ class Act(ctypes.Structure):
     _fields_ = [("rows_cap", ctypes.c_int64), ("rows", ctypes.c_void_p), ("F", ctypes.c_int32), ("dtype", ctypes.c_int),
                 ("activation", ctypes.c_int32), ("p", ctypes.c_double), ("rng", ctypes.c_void_p),
                 ("ld_in", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("ld_grad", ctypes.c_int64)]
+
+
+class Q4(ctypes.Structure):
+    """moe_q4_t: sizes, types and row pitches of a product with 4-bit weights."""
+    _fields_ = [("E", ctypes.c_int32), ("rows_cap", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("activation", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
 class RowSegment(ctypes.Structure):
@@ -143,6 +151,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_act_dropout.restype = st
     lib.moe_act_dropout_backward.argtypes = [P(Act), vp, vp, vp, vp, vp, vp]
     lib.moe_act_dropout_backward.restype = st
+    i32 = ctypes.c_int32
+    lib.moe_q4_packed_size.argtypes = [i32, i32, i32, i32]
+    lib.moe_q4_packed_size.restype = sz
+    lib.moe_q4_quantize.argtypes = [i32, i32, i32, i32, ctypes.c_int, vp, vp, vp, vp]
+    lib.moe_q4_quantize.restype = st
+    lib.moe_q4_pack.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp]
+    lib.moe_q4_pack.restype = st
+    lib.moe_q4_dequantize.argtypes = [i32, i32, i32, i32, vp, ctypes.c_int, vp, vp]
+    lib.moe_q4_dequantize.restype = st
+    lib.moe_q4_workspace_size.argtypes = []
+    lib.moe_q4_workspace_size.restype = sz
+    lib.moe_q4_matmul.argtypes = [P(Q4), vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_q4_matmul.restype = st
+    lib.moe_expert_ffn_q4.argtypes = [P(Shape), P(IO), i32, vp, vp, vp, sz, vp, sz, ctypes.c_int, vp]
+    lib.moe_expert_ffn_q4.restype = st
     lib.moe_debug_activation.argtypes = [ctypes.c_int, vp, vp, ctypes.c_int64, vp]
     lib.moe_debug_activation.restype = st
     lib.moe_debug_timeout_probe.argtypes = [vp, sz, vp]
@@ -308,6 +331,35 @@ def moe_act_dropout_backward(m: Act, dy, u, gate, du, dgate=None, stream=0) -> i
     return load_library().moe_act_dropout_backward(ctypes.byref(m), dy, u, gate, du, dgate, stream)
 
 
+def moe_q4_packed_size(E: int, K: int, N: int, group: int) -> int:
+    return load_library().moe_q4_packed_size(E, K, N, group)
+
+
+def moe_q4_quantize(E, K, N, group, dtype, W, codes, scales, stream=0) -> int:
+    return load_library().moe_q4_quantize(E, K, N, group, dtype, W, codes, scales, stream)
+
+
+def moe_q4_pack(E, K, N, group, codes, scales, packed, stream=0) -> int:
+    return load_library().moe_q4_pack(E, K, N, group, codes, scales, packed, stream)
+
+
+def moe_q4_dequantize(E, K, N, group, packed, dtype, W, stream=0) -> int:
+    return load_library().moe_q4_dequantize(E, K, N, group, packed, dtype, W, stream)
+
+
+def moe_q4_workspace_size() -> int:
+    return load_library().moe_q4_workspace_size()
+
+
+def moe_q4_matmul(m: Q4, offsets, x, packed, bias, y, ws, ws_bytes, stream=0) -> int:
+    return load_library().moe_q4_matmul(ctypes.byref(m), offsets, x, packed, bias, y, ws, ws_bytes, stream)
+
+
+def moe_expert_ffn_q4(shape, io, group, W1q, W2q, ws, ws_bytes, q4_ws, q4_ws_bytes, combine=1, stream=0) -> int:
+    return load_library().moe_expert_ffn_q4(ctypes.byref(shape), ctypes.byref(io), group, W1q, W2q, ws, ws_bytes, q4_ws,
+                                            q4_ws_bytes, int(combine), stream)
+
+
 def moe_debug_activation(activation: int, u, out, n: int, stream=0) -> int:
     return load_library().moe_debug_activation(int(activation), u, out, int(n), stream)
 
@@ -389,6 +441,25 @@ class MoEBuffers:
         return _check(moe_expert_ffn(self.shape, self.io, self.ws_ptr, self.ws_bytes, int(fuse_combine), self.stream()),
                       "moe_expert_ffn")
 
+    def expert_ffn_q4(self, W1, W2, q4_ws, combine=True):
+        """expert_ffn with 4-bit weights: W1 and W2 are ``Q4Weights`` of one group size (W1 H by F, W2 F by H),
+        q4_ws a ``q4_workspace()``.  The layer's biases and activation apply; inputs W1 and W2 are not read."""
+        s = self.shape
+        for name, w, K, N in (("W1", W1, s.H, s.F), ("W2", W2, s.F, s.H)):
+            if (w.E, w.K, w.N) != (s.E, K, N) or w.group != W1.group or w.packed.device != self.ws.device:
+                raise ValueError(f"{name} must hold [{s.E}, {K}, {N}] in groups of {W1.group} on {self.ws.device}")
+        if q4_ws.device != self.ws.device:
+            raise ValueError(f"q4_ws must be on {self.ws.device}")
+        return _check(moe_expert_ffn_q4(s, self.io, W1.group, W1.packed.data_ptr(), W2.packed.data_ptr(), self.ws_ptr,
+                                        self.ws_bytes, q4_ws.data_ptr(), q4_ws.numel() * q4_ws.element_size(), int(combine),
+                                        self.stream()), "moe_expert_ffn_q4")
+
+    def forward_q4(self, W1, W2, q4_ws):
+        """The layer's forward pass with its experts in 4 bits: route, permute, expert_ffn_q4 with the combine."""
+        self.route()
+        self.permute()
+        return self.expert_ffn_q4(W1, W2, q4_ws)
+
     def combine(self):
         return _check(moe_combine(self.shape, self.io, self.ws_ptr, self.ws_bytes, self.stream()), "moe_combine")
 
@@ -451,7 +522,8 @@ class MoEBuffers:
 
 
 # The operators on torch tensors, imported on first use: the binding itself loads without torch.
-_OPERATORS = ("grouped_matmul", "grouped_wgrad", "act_dropout", "act_dropout_backward")
+_OPERATORS = ("grouped_matmul", "grouped_wgrad", "act_dropout", "act_dropout_backward", "Q4Weights", "q4_quantize",
+              "q4_workspace", "q4_matmul")
 
 
 def __getattr__(name):

@@ -521,6 +521,56 @@ moe_status_t moe_expert_ffn(const moe_shape_t* shape, const moe_io_t* io, void* 
   return do_ffn(shape, io, ws, fuse_combine ? 1 : 0, stream);
 }
 
+moe_status_t moe_expert_ffn_q4(const moe_shape_t* shape, const moe_io_t* io, int32_t group, const void* W1q,
+                               const void* W2q, void* ws, size_t ws_bytes, void* q4_ws, size_t q4_ws_bytes, int combine,
+                               cudaStream_t stream) {
+  NvtxRange nvtx_range("moe_expert_ffn_q4");
+  g_launches = 0;
+  moe_status_t st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (io == nullptr) return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(shape, ws, ws_bytes)) != MOE_OK) return st;
+  const WsLayout L = ws_layout(*shape);
+  moe_q4_t m{};
+  m.E = shape->E;
+  m.rows_cap = L.rows;
+  m.K = shape->H;
+  m.N = shape->F;
+  m.group = group;
+  m.dtype = m.out_dtype = shape->dtype;
+  m.activation = shape->activation;
+  if ((st = check_q4_matmul(&m, q4_ws, q4_ws_bytes)) != MOE_OK) return st;
+  moe_q4_t m2 = m;
+  m2.K = shape->F;
+  m2.N = shape->H;
+  m2.out_dtype = MOE_DTYPE_F32;
+  m2.activation = MOE_ACT_NONE;
+  if ((st = check_q4_matmul(&m2, q4_ws, q4_ws_bytes)) != MOE_OK) return st;
+  const bool ec = shape->routing == MOE_ROUTING_EXPERT_CHOICE;
+  if (shape->T == 0) return MOE_OK;
+  if (null_any({W1q, W2q, io->topk_w}) || (combine && (io->out == nullptr || (ec && io->topk_idx == nullptr))))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(W1q) || !aligned16(W2q) || !aligned16(io->b1) || !aligned16(io->b2) || (combine && !aligned16(io->out)))
+    return MOE_ERR_INVALID_ARG;
+  int32_t* status = at<int32_t>(ws, L.status);
+  const int32_t* offsets = at<int32_t>(ws, L.offsets);
+  if ((st = cuda_status(launch_q4_matmul(m, offsets, at<void>(ws, L.x_perm), W1q, io->b1, at<void>(ws, L.h), q4_ws, status,
+                                         stream))) != MOE_OK)
+    return st;
+  ++g_launches;
+  if ((st = cuda_status(launch_q4_matmul(m2, offsets, at<void>(ws, L.h), W2q, io->b2, at<float>(ws, L.y), q4_ws, status,
+                                         stream))) != MOE_OK)
+    return st;
+  ++g_launches;
+  if (!combine) return MOE_OK;
+  ++g_launches;
+  if (ec)
+    return cuda_status(launch_ec_combine(at<float>(ws, L.y), io->topk_idx, io->topk_w, shape->T, shape->E, L.ec_cap,
+                                         shape->H, io->out, stream));
+  return cuda_status(launch_combine(at<float>(ws, L.y), at<int32_t>(ws, L.row_of), io->topk_w, shape->T, shape->H,
+                                    shape->k, io->out, stream));
+}
+
 moe_status_t moe_combine(const moe_shape_t* shape, const moe_io_t* io, void* ws, size_t ws_bytes, cudaStream_t stream) {
   NvtxRange nvtx_range("moe_combine");
   g_launches = 0;

@@ -1,5 +1,5 @@
 """The experts' operators on torch tensors: matrix products grouped by expert, the activation with gate and
-dropout between them, and their gradients.
+dropout between them, their gradients, and products with 4-bit weights.
 
 Like ``MoEBuffers`` these functions only marshal arguments: they check shapes, types and devices, allocate
 what the caller did not pass, and call the C entry point of the same meaning (``moe_grouped_matmul`` ...) on
@@ -195,3 +195,86 @@ def act_dropout_backward(dy, u, gate=None, activation="gelu", p: float = 0.0, rn
     _call("moe_act_dropout_backward", u.device, _moe.load_library().moe_act_dropout_backward, ctypes.byref(m), dy.data_ptr(),
           u.data_ptr(), None if gate is None else gate.data_ptr(), du.data_ptr(), None if dgate is None else dgate.data_ptr())
     return du if gate is None else (du, dgate)
+
+
+def q4_quantize(W, group: int = 64):
+    """4-bit codes and scales of ``W [E, K, N]`` (bf16 or f32, contiguous): ``(codes uint8 [E, N, K / 2], scales bf16
+    [E, K / group, N])``, with ``W[e, k, n]`` near ``scales[e, k // group, n] * (code - 8)`` and the code of an even k
+    in the low half of its byte.  Symmetric: the scale is max |w| / 7 of the group, codes round to the nearest."""
+    _need(W.dim() == 3, "W must have three dimensions")
+    code = _dtype(W, "W")
+    _need(W.is_contiguous(), "W must be contiguous")
+    E, K, N = W.shape
+    _need(group in (32, 64, 128) and K % group == 0 and K > 0, "group must be 32, 64 or 128 and divide K")
+    q = torch.empty((E, N, K // 2), dtype=torch.uint8, device=W.device)
+    s = torch.empty((E, K // group, N), dtype=torch.bfloat16, device=W.device)
+    _call("moe_q4_quantize", W.device, _moe.load_library().moe_q4_quantize, E, K, N, group, code, W.data_ptr(), q.data_ptr(),
+          s.data_ptr())
+    return q, s
+
+
+class Q4Weights:
+    """Expert weights ``[E, K, N]`` in 4 bits, laid out for ``q4_matmul`` (once, from codes and scales as
+    ``q4_quantize`` makes them; those are not kept)."""
+
+    def __init__(self, codes, scales):
+        device = codes.device
+        _need(codes.dim() == 3 and codes.dtype == torch.uint8, "codes must be a uint8 [E, N, K / 2] tensor")
+        _need(scales.dim() == 3, "scales must have three dimensions")
+        self.E, self.N, self.K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
+        groups = scales.shape[1]
+        _need(groups > 0 and self.K % groups == 0 and self.K // groups in (32, 64, 128),
+              f"scales must be [E, K / group, N] with a group of 32, 64 or 128, not {tuple(scales.shape)} for K = {self.K}")
+        self.group = self.K // groups
+        qptr = _dense(codes, "codes", device, torch.uint8, codes.shape)
+        sptr = _dense(scales, "scales", device, torch.bfloat16, (self.E, groups, self.N))
+        size = _moe.moe_q4_packed_size(self.E, self.K, self.N, self.group)
+        if size == 0:
+            raise _moe.MoEError(_moe.MOE_ERR_UNSUPPORTED, "moe_q4_packed_size")
+        self.packed = torch.empty(size, dtype=torch.uint8, device=device)
+        _call("moe_q4_pack", device, _moe.load_library().moe_q4_pack, self.E, self.K, self.N, self.group, qptr, sptr,
+              self.packed.data_ptr())
+
+    def dequantize(self, dtype=torch.bfloat16):
+        """The weights ``[E, K, N]`` as they are computed with, rounded to dtype (exact in float32)."""
+        W = torch.empty((self.E, self.K, self.N), dtype=dtype, device=self.packed.device)
+        _call("moe_q4_dequantize", W.device, _moe.load_library().moe_q4_dequantize, self.E, self.K, self.N, self.group,
+              self.packed.data_ptr(), _dtype(W, "W"), W.data_ptr())
+        return W
+
+
+def q4_workspace(device="cuda"):
+    """A workspace for ``q4_matmul`` calls that follow each other on one stream; it serves every size."""
+    return torch.zeros(_moe.moe_q4_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def q4_matmul(x, W: Q4Weights, offsets, bias=None, activation=None, out=None, out_dtype=None, ws=None):
+    """``out[r] = act(x[r] @ W[e] + bias[e])`` for the rows ``offsets[e] <= r < offsets[e + 1]`` of every expert.
+
+    x ``[rows, K]`` bf16 or f32 (rows may be strided), W a ``Q4Weights``, bias ``[E, N]`` of x's type or None,
+    activation "gelu", "silu" or None, ``out`` ``[rows, N]`` of x's type or ``out_dtype`` (f32 or x's; rows may be
+    strided); rows past ``offsets[E]`` are not written.  Made for a few rows an expert, right for any.  ws: a
+    ``q4_workspace()`` that no call on another stream uses meanwhile (made for the call when not given); a bad
+    offset is recorded in its first word (``moe_get_device_status(ws.data_ptr())``)."""
+    device = x.device
+    code = _dtype(x, "x")
+    ldx = _rows(x, "x", device)
+    optr, E = _offsets(offsets, device)
+    _need(E == W.E, f"offsets has {E} experts, W {W.E}")
+    _need(x.shape[1] == W.K, f"x must have {W.K} columns, not {x.shape[1]}")
+    _need(W.packed.device == device, f"W is on {W.packed.device}, expected {device}")
+    bptr = _dense(bias, "bias", device, x.dtype, (E, W.N))
+    if out is None:
+        out = torch.empty((x.shape[0], W.N), dtype=out_dtype or x.dtype, device=device)
+    else:
+        _need(tuple(out.shape) == (x.shape[0], W.N), f"out must have shape {(x.shape[0], W.N)}, not {tuple(out.shape)}")
+        _need(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
+    ldy = _rows(out, "out", device)
+    if ws is None:
+        ws = q4_workspace(device)
+    else:
+        _need(ws.device == device and ws.is_contiguous(), f"ws must be a contiguous tensor on {device}")
+    m = _moe.Q4(E, x.shape[0], W.K, W.N, W.group, code, _dtype(out, "out"), _activation(activation), ldx, ldy)
+    _call("moe_q4_matmul", device, _moe.load_library().moe_q4_matmul, ctypes.byref(m), optr, x.data_ptr(), W.packed.data_ptr(),
+          bptr, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    return out

@@ -157,3 +157,117 @@ def test_philox_known_answers():
 def test_act_tensor_checks(call, message):
     with pytest.raises(ValueError, match=message):
         call()
+
+
+# ---------------------------------------------------------------- 4-bit weights
+WS = 1 << 30
+
+
+def q4(**kw):
+    d = dict(E=4, rows_cap=10, K=128, N=100, group=64, dtype=1, out_dtype=1, activation=-1, ldx=0, ldy=0)
+    d.update(kw)
+    return moe.Q4(**d)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(E=0), moe.MOE_ERR_INVALID_ARG), (dict(E=257), moe.MOE_ERR_INVALID_ARG), (dict(rows_cap=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(K=0), moe.MOE_ERR_INVALID_ARG), (dict(N=0), moe.MOE_ERR_INVALID_ARG), (dict(group=16), moe.MOE_ERR_INVALID_ARG),
+    (dict(group=0), moe.MOE_ERR_INVALID_ARG), (dict(dtype=2), moe.MOE_ERR_INVALID_ARG), (dict(out_dtype=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(activation=2), moe.MOE_ERR_INVALID_ARG), (dict(activation=-2), moe.MOE_ERR_INVALID_ARG),
+    (dict(ldx=120), moe.MOE_ERR_INVALID_ARG), (dict(ldy=99), moe.MOE_ERR_INVALID_ARG), (dict(K=96), moe.MOE_ERR_UNSUPPORTED),
+    (dict(K=1 << 25), moe.MOE_ERR_UNSUPPORTED), (dict(N=(1 << 24) + 1), moe.MOE_ERR_UNSUPPORTED), (dict(ldx=132), moe.MOE_ERR_UNSUPPORTED),
+    (dict(dtype=0, out_dtype=0, ldx=130), moe.MOE_ERR_UNSUPPORTED), (dict(dtype=0), moe.MOE_ERR_UNSUPPORTED),
+    (dict(rows_cap=(1 << 31) - 1024), moe.MOE_ERR_UNSUPPORTED), (dict(ldy=1 << 31), moe.MOE_ERR_UNSUPPORTED),
+])
+def test_q4_sizes(bad, code):
+    assert moe.moe_q4_matmul(q4(**bad), FAKE, FAKE, FAKE, None, FAKE, FAKE, WS) == code
+    assert moe.moe_last_launch_count() == 0
+
+
+def test_q4_pointers_and_workspace():
+    ok = [FAKE, FAKE, FAKE, None, FAKE, FAKE]
+    for i in (0, 1, 2, 4, 5):  # offsets, x, packed, y, ws
+        for p in (None, FAKE + 1):
+            args = list(ok)
+            args[i] = p
+            assert moe.moe_q4_matmul(q4(), *args, WS) == moe.MOE_ERR_INVALID_ARG, (i, p)
+    assert moe.moe_q4_matmul(q4(), FAKE, FAKE + 8, FAKE, None, FAKE, FAKE, WS) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_q4_matmul(q4(), FAKE, FAKE, FAKE, FAKE + 1, FAKE, FAKE, WS) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_q4_matmul(q4(), *ok[:5], FAKE + 128, WS) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_q4_matmul(q4(), *ok, moe.moe_q4_workspace_size() - 1) == moe.MOE_ERR_WORKSPACE
+    assert moe.moe_q4_matmul(q4(rows_cap=0), None, None, None, None, None, FAKE, WS) == moe.MOE_OK
+    assert moe.load_library().moe_q4_matmul(None, *ok, WS, None) == moe.MOE_ERR_INVALID_ARG
+    assert ctypes.sizeof(moe.Q4) == 56 and moe.Q4.ldx.offset == 40
+
+
+def test_q4_layout_calls():
+    assert moe.moe_q4_packed_size(2, 128, 16, 64) == 2 * (1024 + 64)
+    assert moe.moe_q4_packed_size(1, 160, 17, 32) == 2 * 2 * (1024 + 128)  # two steps of 128, two tiles of 16
+    for E, K, N, group, code in ((0, 128, 8, 64, 1), (1, 128, 8, 48, 1), (1, 0, 8, 64, 1), (1, 128, 0, 64, 1), (1, 96, 8, 64, 2)):
+        assert moe.moe_q4_packed_size(E, K, N, group) == 0
+        assert moe.moe_q4_pack(E, K, N, group, FAKE, FAKE, FAKE) == code
+        assert moe.moe_q4_quantize(E, K, N, group, 1, FAKE, FAKE, FAKE) == code
+        assert moe.moe_q4_dequantize(E, K, N, group, FAKE, 1, FAKE) == code
+    for bad in (None, FAKE + 1):
+        for i in range(3):
+            args = [FAKE] * 3
+            args[i] = bad
+            assert moe.moe_q4_pack(1, 128, 8, 64, *args) == moe.MOE_ERR_INVALID_ARG
+            assert moe.moe_q4_quantize(1, 128, 8, 64, 1, *args) == moe.MOE_ERR_INVALID_ARG
+        assert moe.moe_q4_dequantize(1, 128, 8, 64, bad, 1, FAKE) == moe.MOE_ERR_INVALID_ARG
+        assert moe.moe_q4_dequantize(1, 128, 8, 64, FAKE, 1, bad) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_q4_quantize(1, 128, 8, 64, 2, FAKE, FAKE, FAKE) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_q4_dequantize(1, 128, 8, 64, FAKE, 7, FAKE) == moe.MOE_ERR_INVALID_ARG
+
+
+def test_q4_layer_checks():
+    shape = moe.make_shape(16, 128, 4, 2, 192, dtype="bf16")
+    io = moe.IO(*([FAKE] * 14))
+
+    def call(shape=shape, io=io, group=64, W1=FAKE, W2=FAKE, ws=FAKE, bytes=WS, q4ws=FAKE, q4bytes=WS, combine=1):
+        return moe.moe_expert_ffn_q4(shape, io, group, W1, W2, ws, bytes, q4ws, q4bytes, combine)
+
+    assert call(group=128) == moe.MOE_ERR_UNSUPPORTED  # does not divide F
+    assert call(group=48) == moe.MOE_ERR_INVALID_ARG
+    assert call(bytes=100) == moe.MOE_ERR_WORKSPACE and call(q4bytes=100) == moe.MOE_ERR_WORKSPACE
+    for bad in (dict(W1=None), dict(W2=None), dict(W1=FAKE + 8), dict(ws=None), dict(q4ws=None), dict(q4ws=FAKE + 64)):
+        assert call(**bad) == moe.MOE_ERR_INVALID_ARG, bad
+    no_out = moe.IO(*([FAKE] * 14))
+    no_out.out = None
+    assert call(io=no_out) == moe.MOE_ERR_INVALID_ARG
+    assert call(shape=moe.make_shape(0, 128, 4, 2, 192, dtype="bf16")) == moe.MOE_OK
+    assert moe.moe_last_launch_count() == 0
+
+
+def q4_weights(E=2, K=128, N=8, group=64):
+    w = object.__new__(moe.Q4Weights)
+    w.E, w.K, w.N, w.group, w.packed = E, K, N, group, torch.zeros(moe.moe_q4_packed_size(E, K, N, group), dtype=torch.uint8)
+    return w
+
+
+U8, I32 = torch.uint8, torch.int32
+
+
+@pytest.mark.parametrize("call,message", [
+    (lambda: moe.q4_quantize(z(128, 8)), "three dimensions"),
+    (lambda: moe.q4_quantize(z(1, 128, 8, dtype=torch.float16)), "float32 or bfloat16"),
+    (lambda: moe.q4_quantize(z(1, 128, 8), 48), "group"),
+    (lambda: moe.q4_quantize(z(1, 96, 8), 64), "group"),
+    (lambda: moe.q4_quantize(z(1, 8, 128).mT, 64), "contiguous"),
+    (lambda: moe.q4_quantize(z(1, 128, 8), 64), "needs CUDA tensors"),
+    (lambda: moe.Q4Weights(z(1, 8, 64), z(1, 2, 8)), "codes must be"),
+    (lambda: moe.Q4Weights(z(1, 8, 64, dtype=U8), z(1, 3, 8)), "scales must be"),
+    (lambda: moe.Q4Weights(z(1, 8, 64, dtype=U8), z(1, 2, 9)), "scales must have shape"),
+    (lambda: moe.Q4Weights(z(1, 8, 64, dtype=U8), z(1, 2, 8, dtype=torch.float32)), "scales must be torch.bfloat16"),
+    (lambda: moe.Q4Weights(z(1, 8, 64, dtype=U8), z(1, 2, 8)), "needs CUDA tensors"),
+    (lambda: moe.q4_matmul(z(4, 128), q4_weights(), z(4, dtype=I32)), "experts"),
+    (lambda: moe.q4_matmul(z(4, 64), q4_weights(), z(3, dtype=I32)), "128 columns"),
+    (lambda: moe.q4_matmul(z(4, 128), q4_weights(), z(3, dtype=I32), bias=z(2, 9)), "bias must have shape"),
+    (lambda: moe.q4_matmul(z(4, 128), q4_weights(), z(3, dtype=I32), activation="relu"), "unknown activation"),
+    (lambda: moe.q4_matmul(z(4, 128), q4_weights(), z(3, dtype=I32), out=z(4, 9), ws=z(1)), "out must have shape"),
+    (lambda: moe.q4_matmul(z(4, 128), q4_weights(), z(3, dtype=I32), out=z(4, 8), out_dtype=torch.float32, ws=z(1)), "another type"),
+    (lambda: moe.q4_matmul(z(4, 128), q4_weights(), z(3, dtype=I32), ws=z(1)), "needs CUDA tensors"),
+])
+def test_q4_tensor_checks(call, message):
+    with pytest.raises(ValueError, match=message):
+        call()
