@@ -529,8 +529,8 @@ typedef struct {
  * weights once).  Errors: MOE_ERR_INVALID_ARG (sizes and pointers as above; rows_cap < 0; a pitch below the row;
  * an unknown type or activation; x not 16-byte aligned, y, bias and offsets below their type's alignment; ws null
  * or misaligned), MOE_ERR_UNSUPPORTED (K not a multiple of group, ldx as above, fp32 x with a bf16 y, K or N above
- * 2^24, a pitch of 2^31 or more, rows_cap >= 2^31 - 1024), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.
- * 1 launch; none for rows_cap = 0. */
+ * 2^24, a pitch of 2^31 or more, rows_cap >= 2^31 - 1024, more than 2^31 pieces of 32 rows, 256 columns and 128
+ * inputs), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.  1 launch; none for rows_cap = 0. */
 MOE_API size_t moe_q4_workspace_size(void);
 MOE_API moe_status_t moe_q4_matmul(const moe_q4_t* m, const int32_t* offsets, const void* x, const void* packed,
                                    const void* bias, void* y, void* ws, size_t ws_bytes, cudaStream_t stream);

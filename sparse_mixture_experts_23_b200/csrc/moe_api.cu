@@ -554,11 +554,11 @@ moe_status_t moe_expert_ffn_q4(const moe_shape_t* shape, const moe_io_t* io, int
     return MOE_ERR_INVALID_ARG;
   int32_t* status = at<int32_t>(ws, L.status);
   const int32_t* offsets = at<int32_t>(ws, L.offsets);
-  if ((st = cuda_status(launch_q4_matmul(m, offsets, at<void>(ws, L.x_perm), W1q, io->b1, at<void>(ws, L.h), q4_ws, status,
+  if ((st = cuda_status(launch_q4_matmul(m, offsets, at<void>(ws, L.x_perm), W1q, io->b1, at<void>(ws, L.h), status,
                                          stream))) != MOE_OK)
     return st;
   ++g_launches;
-  if ((st = cuda_status(launch_q4_matmul(m2, offsets, at<void>(ws, L.h), W2q, io->b2, at<float>(ws, L.y), q4_ws, status,
+  if ((st = cuda_status(launch_q4_matmul(m2, offsets, at<void>(ws, L.h), W2q, io->b2, at<float>(ws, L.y), status,
                                          stream))) != MOE_OK)
     return st;
   ++g_launches;

@@ -347,6 +347,6 @@ cudaError_t launch_grouped_wgrad_sm100(const GroupedArgs& a, const void* dy, flo
 moe_status_t check_q4_matmul(const moe_q4_t* m, const void* ws, size_t ws_bytes);
 // Arguments that have passed them, rows_cap > 0.  1 launch.
 cudaError_t launch_q4_matmul(const moe_q4_t& m, const int32_t* offsets, const void* x, const void* packed, const void* bias,
-                             void* y, void* ws, int32_t* status, cudaStream_t st);
+                             void* y, int32_t* status, cudaStream_t st);
 
 }  // namespace moe

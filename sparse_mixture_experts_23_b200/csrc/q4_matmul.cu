@@ -4,19 +4,29 @@
 // 4 bits and a scale for each group of G inputs of an output column.)
 //
 // Bound: reading the weights from HBM (half a byte each), as decode with bf16 weights is by four times the bytes.
-// Mathematics: a group's sum  d[n,r] = sum_{k in group} (c - 8) x[r,k]  runs on mma.sync m16n8k16 with the weights
-// as the 16-row operand (c - 8 is exact in bf16) and eight rows of x as the 8-column one, and joins the fp32
-// accumulator as  acc += s d:  no weight is rounded, and tensor-core sums (which cut) are at most 64 terms long.
-// fp32 rows are split exactly into three bf16 parts (8 bits of the significand each), three products a step.
-// mma.sync rather than tcgen05: at up to 32 rows the product is 1 / 8 of what the tensor pipe could do in the time
-// that the weights take, and its register operand is what unpacking produces; tcgen05 wants them in shared memory.
+// Mathematics: a sum over up to 64 inputs of a group,  d[n,r] = sum_k (c - 8) x[r,k],  runs on mma.sync m16n8k16 with
+// the weights as the 16-row operand and eight rows of x as the 8-column one, and joins the fp32 accumulator as
+// acc += s d:  no weight is rounded, and tensor-core sums (which cut) are short.  Unpacking sets the pace next to the
+// bytes: one shift and one logic instruction make 16 + c of two codes.  The -24 is not taken from every weight but
+// once for a warp's 32 columns, d = sum (-24) x + sum (16 + c) x, the first sum being one more product with a constant
+// operand that the second starts from; what cancels is five times the result's size, so about 2^-21 of the summed
+// magnitudes are lost.  An infinity in x (or an overflow of the larger terms) would leave NaN there: a sum that is not
+// finite is computed again term by term.  For fp32 rows 24 is subtracted from each unpacked weight (exact in bf16),
+// and the rows are split exactly into three bf16 parts (8 bits of the significand each), three products a step.
+// mma.sync rather than tcgen05: at up to 16 rows the product is a small part of what the tensor pipe could do in the
+// time that the weights take, and its register operand is what unpacking produces.
 //
-// Layout (moe_q4_pack): 16 columns x 128 inputs make a block of 1024 bytes of codes in the order of the
-// mma's register operand, then the block's scales; the blocks of up to 16 column tiles at one 128-input step lie
-// together, so a CTA's step is one contiguous run of up to 18 KB that one bulk copy brings.
-// Split: work is (256-column strip of an expert, up to 32 rows of it) x steps of 128 inputs; the steps of all of it
-// laid end to end are shared evenly over one CTA per SM.  A CTA that holds part of a strip's steps leaves its
-// fp32 sums in the workspace, and the last one to finish adds them in CTA order (the same bits every run).
+// Layout (moe_q4_pack): 16 columns (a tile) x 128 inputs (a step) are 1024 bytes of codes in the order of the mma's
+// register operand; a block holds two tiles of a step and their scales, and the blocks of a pair of tiles follow each
+// other along K.
+// Split: a piece of work is two tiles of an expert's block of up to 16 rows, over all of K.  The pieces are shared over
+// one CTA per SM, and its 16 warps work alone: each streams its piece's blocks through a ring of its own (16-byte
+// asynchronous copies, 9 KB in flight a warp, each lane the codes that it will read itself) and reads x through L1,
+// once for its two tiles.  Where a CTA has fewer pieces than warps (or an uneven number), 2 to 16 warps share a piece's
+// steps and add their sums in shared memory, in order.  Nothing crosses a CTA: with K split over CTAs, joining parts
+// through global memory took 4 to 5 us each of a call that streams for 10; with stages and x shared by a CTA's warps,
+// the waits for one another and a fragment of x for every tile took as long as the bytes; and bulk copies of 1 KB are
+// too slow: an SM issues one in about 64 clocks.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -31,28 +41,21 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kWarps = 16;              // consumer warps: one 16-column tile each
-constexpr int kRows = 32;               // rows of a work item (four mma column groups)
-constexpr int kStepK = 128;             // inputs of a pipeline step
-constexpr int kThreadsQ4 = 32 * (kWarps + 1);
-constexpr int kXPitch = kStepK * 2 + 64;  // bytes between staged bf16 rows: reads of 8 rows x 16 bytes miss no bank twice
-constexpr int kMaxCtas = 160;
-constexpr size_t kCounterOff = 256, kPartialOff = 4096;
-constexpr size_t kPartialBytes = (size_t)kWarps * (kRows / 8) * 32 * 16;  // fp32 sums of a 256 x 32 strip
-constexpr size_t kQ4WsBytes = kPartialOff + (size_t)kMaxCtas * 2 * kPartialBytes;
+constexpr int kWarps = 16;     // of a CTA
+constexpr int kRows = 16;      // rows of a piece (two mma column groups)
+constexpr int kStepK = 128;    // inputs of a step
+constexpr int kStages = 5;     // of a warp's ring, each a block
+constexpr size_t kQ4WsBytes = 256;  // the error word
 
-__host__ __device__ constexpr int block_bytes(int group) { return 1024 + (kStepK / group) * 32; }
+// two tiles' codes, then their scales: for each group, 8 words of the scales of columns g and g + 8
+__host__ __device__ constexpr int block_bytes(int group) { return 2 * (1024 + (kStepK / group) * 32); }
 
 struct Q4Shape {  // the packed layout of one expert
-  int tiles, steps, blk;
+  int pairs, steps, blk;
   __host__ __device__ Q4Shape(int K, int N, int group)
-      : tiles((N + 15) / 16), steps((K + kStepK - 1) / kStepK), blk(block_bytes(group)) {}
-  __host__ __device__ size_t expert_bytes() const { return (size_t)tiles * steps * blk; }
-  __host__ __device__ int strip_tiles(int strip) const { return tiles - strip * kWarps < kWarps ? tiles - strip * kWarps : kWarps; }
-  // first block of a strip's step
-  __host__ __device__ size_t at(int strip, int step) const {
-    return ((size_t)strip * kWarps * steps + (size_t)step * strip_tiles(strip)) * blk;
-  }
+      : pairs((N + 31) / 32), steps((K + kStepK - 1) / kStepK), blk(block_bytes(group)) {}
+  __host__ __device__ size_t expert_bytes() const { return (size_t)pairs * steps * blk; }
+  __host__ __device__ size_t at(int pair, int step) const { return ((size_t)pair * steps + step) * blk; }
 };
 
 struct Q4Args {
@@ -62,17 +65,18 @@ struct Q4Args {
   const void* bias;
   void* y;
   int32_t* status;
-  unsigned* counters;
-  float4* partials;
   long long rows_cap, ldx, ldy;
   int E, K, N, act, bf16_out;
-  long long wait_limit;
+  int steps, pairs;  // of one expert's packed weights
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -84,79 +88,113 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-// all consumer threads meet; true when every one of them says so
-__device__ __forceinline__ bool consumers_all(bool ok) {
-  int r;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\nbarrier.red.and.pred q, 1, %2, p;\nselp.b32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((int)ok), "n"(32 * kWarps)
-      : "memory");
-  return r != 0;
+// the warps of a team meet
+__device__ __forceinline__ void team_sync(int team, int warps) {
+  asm volatile("barrier.sync %0, %1;\n" ::"r"(1 + team), "r"(32 * warps) : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// The eight codes of a word (four in each half) as bf16 pairs: 0x4300 | c is 128 + c in bf16 (step 1 there), and
-// taking 136 away is exact.
-__device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t (&a)[4]) {
-  const __nv_bfloat162 bias = __halves2bfloat162(__float2bfloat16_rn(136.f), __float2bfloat16_rn(136.f));
-#pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    const uint32_t v = ((w >> (4 * f)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), bias);
-    a[f] = *reinterpret_cast<const uint32_t*>(&h);
-  }
+// d = a b + c
+__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-
-// One step of a warp's tile: GP groups a step, P bf16 planes of x, RB groups of 8 rows, k32 blocks of 32 inputs.
-template <int GP, int P, int RB>
-__device__ __forceinline__ void q4_step(float (&acc)[kRows / 8][4], uint32_t wblk, uint32_t xs, int k32, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-  const uint32_t xrow = xs + (uint32_t)(g * kXPitch + t * 16);
+// The eight codes of a word (four in each half) as bf16 pairs: 0x4180 | c << 3 is 16 + c in bf16.  One three-input
+// logic instruction a pair, its two constants in registers.  EXACT: less 24, which leaves c - 8.
+struct Unpack {
+  uint32_t mask, magic;
+  __device__ __forceinline__ Unpack() { asm volatile("mov.b32 %0, 0x00780078;\nmov.b32 %1, 0x41804180;\n" : "=r"(mask), "=r"(magic)); }
+  template <bool EXACT>
+  __device__ __forceinline__ void run(uint32_t w, uint32_t (&a)[4]) const {
+    const __nv_bfloat162 off = __halves2bfloat162(__float2bfloat16_rn(24.f), __float2bfloat16_rn(24.f));
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    if (2 * u >= k32) break;
-    const uint4 wv = lds128(wblk + u * 512 + lane * 16);
-    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
-    float d[RB][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (2 * u + h >= k32) break;
-      uint32_t a0[4], a1[4];
-      unpack_codes(ww[2 * h], a0);
-      unpack_codes(ww[2 * h + 1], a1);
-      if (GP == 4 || h == 0) {
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) d[rb][0] = d[rb][1] = d[rb][2] = d[rb][3] = 0.f;
-      }
-#pragma unroll
-      for (int p = P - 1; p >= 0; --p)  // the smallest part of x first
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          const uint4 xv = lds128(xrow + (uint32_t)(p * kRows * kXPitch + rb * 8 * kXPitch + (2 * u + h) * 64));
-          mma16816(d[rb], a0, xv.x, xv.y);
-          mma16816(d[rb], a1, xv.z, xv.w);
-        }
-      if (GP == 4 || h == 1 || 2 * u + 1 == k32) {  // the group's end, or half of a 128-input one
-        const int grp = GP == 4 ? 2 * u + h : (GP == 2 ? u : 0);
-        const uint32_t sc = lds32(wblk + 1024 + grp * 32 + g * 4);
-        const float s0 = __uint_as_float(sc << 16), s1 = __uint_as_float(sc & 0xffff0000u);
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          acc[rb][0] = fmaf(s0, d[rb][0], acc[rb][0]);
-          acc[rb][1] = fmaf(s0, d[rb][1], acc[rb][1]);
-          acc[rb][2] = fmaf(s1, d[rb][2], acc[rb][2]);
-          acc[rb][3] = fmaf(s1, d[rb][3], acc[rb][3]);
-        }
+    for (int f = 0; f < 4; ++f) {
+      asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(a[f]) : "r"(__funnelshift_r(w, w, 4 * f)), "r"(mask), "r"(magic));  // (w & mask) | magic
+      if constexpr (EXACT) {
+        const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a[f]), off);
+        a[f] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
+  }
+};
+
+// A lane's inputs of 64: for each block of 32 and group of 8 rows, 8 inputs of row g of the group
+template <bool F32X, int RB>
+struct XUnit {
+  uint4 v[2][RB][F32X ? 2 : 1];
+  // p[rb]: the lane's place in its row at the step's first input; null for a row that is not there
+  __device__ __forceinline__ void load(const uint8_t* const (&p)[2], int unit, int k32) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int h = 0; h < (F32X ? 2 : 1); ++h) {
+          v[b][rb][h] = make_uint4(0u, 0u, 0u, 0u);
+          if (p[rb] != nullptr && 2 * unit + b < k32)
+            v[b][rb][h] = __ldg(reinterpret_cast<const uint4*>(p[rb] + (2 * unit + b) * (F32X ? 128 : 64) + h * 16));
+        }
+  }
+};
+
+__device__ __forceinline__ void scale_add(float (&acc)[4], uint32_t scales, const float (&d)[4]) {
+  const float s0 = __uint_as_float(scales << 16), s1 = __uint_as_float(scales & 0xffff0000u);
+  acc[0] = fmaf(s0, d[0], acc[0]);
+  acc[1] = fmaf(s0, d[1], acc[1]);
+  acc[2] = fmaf(s1, d[2], acc[2]);
+  acc[3] = fmaf(s1, d[3], acc[3]);
+}
+
+// acc += 64 inputs (unit U of a step) of two tiles: GP groups a step, RB groups of 8 rows.  wl: the lane's codes, sl: its
+// scales.  With one row group each block of 32 is a chain of products of its own
+// (shorter chains); with two the registers hold one chain for both blocks of a group.
+template <int GP, int RB, int U>
+__device__ __forceinline__ void q4_unit(float (&acc)[2][2][4], uint32_t wl, uint32_t sl, const XUnit<false, RB>& x,
+                                        const Unpack& unpack) {
+  constexpr int BG = GP == 4 || RB == 1 ? 1 : 2;
+  const uint32_t minus24[4] = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};
+  const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+  uint4 w[2];
+  uint32_t sc[2][GP == 4 ? 2 : 1];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    w[m] = lds128(wl + m * 1024 + U * 512);
+#pragma unroll
+    for (int i = 0; i < (GP == 4 ? 2 : 1); ++i) sc[m][i] = lds32(sl + (m * GP + (GP == 4 ? 2 * U + i : (GP == 2 ? U : 0))) * 32);
+  }
+  float from[2 / BG][RB][4];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      if (b % BG == 0) mma16816_from(from[b / BG][rb], minus24, x.v[b][rb][0].x, x.v[b][rb][0].y, zero);
+      else mma16816(from[b / BG][rb], minus24, x.v[b][rb][0].x, x.v[b][rb][0].y);
+      mma16816(from[b / BG][rb], minus24, x.v[b][rb][0].z, x.v[b][rb][0].w);
+    }
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    float d[2 / BG][RB][4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t a0[4], a1[4];
+      unpack.run<false>(b ? w[m].z : w[m].x, a0);
+      unpack.run<false>(b ? w[m].w : w[m].y, a1);
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        if (b % BG == 0) mma16816_from(d[b / BG][rb], a0, x.v[b][rb][0].x, x.v[b][rb][0].y, from[b / BG][rb]);
+        else mma16816(d[b / BG][rb], a0, x.v[b][rb][0].x, x.v[b][rb][0].y);
+        mma16816(d[b / BG][rb], a1, x.v[b][rb][0].z, x.v[b][rb][0].w);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2 / BG; ++i)
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) scale_add(acc[m][rb], sc[m][GP == 4 ? i : 0], d[i][rb]);
   }
 }
 
@@ -169,262 +207,255 @@ __device__ __forceinline__ void split3(float x, uint32_t& h, uint32_t& m, uint32
   l = __float_as_uint(r - __uint_as_float(m));
 }
 
-template <bool F32X>
-struct Q4Cfg {
-  static constexpr int kXBytes = F32X ? kRows * kStepK * 4 : kRows * kXPitch;
-  static constexpr int kWBytes = kWarps * block_bytes(32);
-  static constexpr int kStageBytes = kWBytes + kXBytes;
-  static constexpr int kStages = F32X ? 4 : 6;
-  static constexpr int kPlaneOff = kStages * kStageBytes;
-  static constexpr int kPlaneBytes = F32X ? 2 * 3 * kRows * kXPitch : 0;  // double-buffered
-  static constexpr int kBarOff = kPlaneOff + kPlaneBytes;
-  static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;
-  static constexpr int kOffsOff = kMiscOff + 16;
-  static constexpr int kSmemBytes = 128 + kOffsOff + 2 * 260 * 4;
-  static_assert(kSmemBytes <= 232448 && kStageBytes % 128 == 0 && kBarOff % 16 == 0, "shared-memory plan");
-};
+template <int GP, int RB, int U>
+__device__ __forceinline__ void q4_unit(float (&acc)[2][2][4], uint32_t wl, uint32_t sl, const XUnit<true, RB>& x,
+                                        const Unpack& unpack) {
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uint32_t a[2][2][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      unpack.run<true>(lds32(wl + m * 1024 + U * 512 + b * 8), a[m][0]);
+      unpack.run<true>(lds32(wl + m * 1024 + U * 512 + b * 8 + 4), a[m][1]);
+    }
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const uint4 v0 = x.v[b][rb][0], v1 = x.v[b][rb][1];
+      const uint32_t f[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+      uint32_t p[3][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t lo[3], hi[3];
+        split3(__uint_as_float(f[2 * j]), lo[0], lo[1], lo[2]);
+        split3(__uint_as_float(f[2 * j + 1]), hi[0], hi[1], hi[2]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) p[q][j] = __byte_perm(lo[q], hi[q], 0x7632);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 2; q >= 0; --q) {  // the smallest part of x first
+          mma16816(d, a[m][0], p[q][0], p[q][1]);
+          mma16816(d, a[m][1], p[q][2], p[q][3]);
+        }
+        scale_add(acc[m][rb], lds32(sl + (m * GP + (2 * U + b) * GP / 4) * 32), d);
+      }
+    }
+  }
+}
 
-// The work of all CTAs laid end to end: items of `steps` steps, item i of expert e, strip, row block.
-struct Q4Item {
-  int e, strip, row0, rows;
+// a / b for a >= 0, b > 0.  Below 2^20 by a reciprocal: (a + 1/2) / b is at least 1 / (2 b) from a whole number, and the
+// quotient's error below a 2^-21 / b.  The divisions at the start are latency that every call pays.
+__device__ __forceinline__ int idiv(int a, int b) {
+  if (a < (1 << 20)) return (int)__fdividef((float)a + 0.5f, (float)b);
+  return a / b;
+}
+
+struct Q4Piece {
+  int e, pair, row0, rows;
 };
-__device__ __forceinline__ Q4Item find_item(long long i, const int* offs, const int* prefix, int E, int strips) {
-  Q4Item it;
-  it.e = find_segment(prefix, E, (int)(i / strips));
-  const int blocks = prefix[it.e + 1] - prefix[it.e];
-  const long long local = i - (long long)prefix[it.e] * strips;
-  it.strip = (int)(local / blocks);
-  const int rb = (int)(local % blocks);  // row blocks of one strip follow each other: its weights come from L2 then
-  it.row0 = offs[it.e] + rb * kRows;
-  it.rows = min(kRows, offs[it.e + 1] - it.row0);
-  return it;
+// Piece i: the pairs of tiles of a block of rows follow each other, then the blocks of an expert, then the experts.
+__device__ __forceinline__ Q4Piece find_piece(int i, const int* offs, const int* prefix, int E, int pairs) {
+  Q4Piece p;
+  const int block = idiv(i, pairs);
+  p.e = find_segment(prefix, E, block);
+  p.pair = i - block * pairs;
+  p.row0 = offs[p.e] + (block - prefix[p.e]) * kRows;
+  p.rows = min(kRows, offs[p.e + 1] - p.row0);
+  return p;
+}
+
+constexpr int kStageBytes = block_bytes(32);
+constexpr int kSwapOff = kWarps * kStages * kStageBytes;  // 2 KB a warp: sums of a team
+constexpr int kOffsOff = kSwapOff + kWarps * 2048;
+constexpr int kSmemBytes = 128 + kOffsOff + 2 * 260 * 4;
+static_assert(kSmemBytes <= 232448 && kStageBytes % 128 == 0, "shared-memory plan");
+
+// The value of one weight in the packed layout
+__device__ __forceinline__ float q4_value(const uint8_t* expert, const Q4Shape& sh, int group, int k, int n) {
+  const int r = k % kStepK, m = (n >> 4) & 1;
+  const uint8_t* blk = expert + sh.at(n >> 5, k / kStepK);
+  const int lane = (n & 7) * 4 + ((r & 31) >> 3);
+  const int word = ((r & 63) >> 5) * 2 + ((r & 7) >> 2), field = ((r & 3) >> 1) * 2 + ((n >> 3) & 1);
+  const uint32_t turned = *reinterpret_cast<const uint32_t*>(blk + m * 1024 + (r >> 6) * 512 + lane * 16 + word * 4);
+  const uint32_t w = turned >> 3 | turned << 29;
+  const int code = (int)((w >> (16 * (r & 1) + 4 * field)) & 15u);
+  const uint32_t sc = *reinterpret_cast<const uint32_t*>(blk + 2048 + (m * (kStepK / group) + r / group) * 32 + (n & 7) * 4);
+  return (float)(code - 8) * __uint_as_float((n & 8) ? sc & 0xffff0000u : sc << 16);  // 4 by 8 bits: exact
+}
+
+// The sums of a tile's eight rows term by term, for rows that hold an infinity or NaN and for sums that overflow on
+// the way: lane's elements as everywhere, columns g and g + 8 of rows 2t and 2t + 1.
+__device__ __noinline__ float4 sums_term_by_term(const Q4Args& a, const uint8_t* expert, int group, int n0, int row0, int rows, int lane) {
+  const Q4Shape sh(a.K, a.N, group);
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = (lane & 3) * 2 + (j & 1), n = n0 + (lane >> 2) + 8 * (j >> 1);
+    if (r >= rows || n >= a.N) continue;
+    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(a.x) + ((size_t)row0 + r) * a.ldx;
+    for (int k = 0; k < a.K; ++k) v[j] = fmaf(__bfloat162float(x[k]), q4_value(expert, sh, group, k, n), v[j]);
+  }
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// Bias, activation and the store of one lane's four sums: columns n and n + 8 of `rows` of the rows row and row + 1.
+template <bool F32X>
+__device__ __forceinline__ void store_unit(const Q4Args& a, int e, int n, int row, int rows, const float (&s)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int col = n + 8 * (j >> 1);
+    if ((j & 1) >= rows || col >= a.N) continue;
+    float v = s[j];
+    if (a.bias != nullptr)
+      v += F32X ? static_cast<const float*>(a.bias)[(size_t)e * a.N + col]
+                : __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[(size_t)e * a.N + col]);
+    const size_t at = ((size_t)row + (j & 1)) * a.ldy + col;
+    if (a.bf16_out) {
+      if (a.act == MOE_ACT_GELU) v = activate<MOE_ACT_GELU, true>(v);
+      else if (a.act == MOE_ACT_SILU) v = activate<MOE_ACT_SILU, true>(v);
+      static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+    } else {
+      if (a.act == MOE_ACT_GELU) v = activate<MOE_ACT_GELU, false>(v);
+      else if (a.act == MOE_ACT_SILU) v = activate<MOE_ACT_SILU, false>(v);
+      static_cast<float*>(a.y)[at] = v;
+    }
+  }
+}
+
+// A warp starts the copies of a block: each lane the codes that it reads itself, the first lanes the scales.
+template <int GP>
+__device__ __forceinline__ void fill(uint32_t stage, const uint8_t* block, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) copy16(stage + i * 512 + lane * 16, block + i * 512 + lane * 16);
+  if (lane < 4 * GP) copy16(stage + 2048 + lane * 16, block + 2048 + lane * 16);
+}
+
+// acc += steps [k, k1) of a piece, whose block at step k is `block`.
+template <int GP, bool F32X, int RB>
+__device__ __forceinline__ void q4_run(const Q4Args& a, const Q4Piece& p, int k, int k1, const uint8_t* block, uint32_t ring, int lane,
+                                       const Unpack& unpack, float (&acc)[2][2][4]) {
+  constexpr int kBlk = block_bytes(kStepK / GP), ES = F32X ? 4 : 2;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (k + s < k1) fill<GP>(ring + s * kStageBytes, block + (size_t)s * kBlk, lane);
+    copies_commit();
+  }
+  block += (size_t)(kStages - 1) * kBlk;
+  const uint8_t* xp[2] = {nullptr, nullptr};
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    const int r = rb * 8 + (lane >> 2);
+    if (r < p.rows) xp[rb] = a.x + ((size_t)p.row0 + r) * a.ldx * ES + ((size_t)k * kStepK + (lane & 3) * 8) * ES;
+  }
+  XUnit<F32X, RB> x0, x1;
+  x0.load(xp, 0, k < k1 ? (a.K - k * kStepK) >> 5 : 0);
+  uint32_t stage = ring, fresh = ring + (kStages - 1) * kStageBytes;
+  const uint32_t last = fresh;
+  for (; k < k1; ++k) {
+    if (k + kStages - 1 < k1) fill<GP>(fresh, block, lane);  // the stage that the step before has read
+    copies_commit();
+    block += kBlk;
+    copies_wait<kStages - 1>();
+    __syncwarp();  // the scales have come by way of other lanes
+    const uint32_t wl = stage + lane * 16, sl = stage + 2048 + (lane >> 2) * 4;
+    x1.load(xp, 1, (a.K - k * kStepK) >> 5);
+    q4_unit<GP, RB, 0>(acc, wl, sl, x0, unpack);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+      if (xp[rb] != nullptr) xp[rb] += kStepK * ES;
+    x0.load(xp, 0, k + 1 < k1 ? (a.K - (k + 1) * kStepK) >> 5 : 0);
+    q4_unit<GP, RB, 1>(acc, wl, sl, x1, unpack);
+    fresh = stage;
+    stage = stage == last ? ring : stage + kStageBytes;
+    __syncwarp();  // every lane has read the stage
+  }
 }
 
 template <int GP, bool F32X>
-__global__ void __launch_bounds__(kThreadsQ4, 1) q4_matmul_kernel(Q4Args a) {
-  using C = Q4Cfg<F32X>;
+__global__ void __launch_bounds__(32 * kWarps, 1) q4_matmul_kernel(const __grid_constant__ Q4Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~(uintptr_t)127);
   const uint32_t sbase = smem_u32(smem);
-  auto full_bar = [&](int s) { return sbase + C::kBarOff + 8u * s; };
-  auto empty_bar = [&](int s) { return sbase + C::kBarOff + 8u * (C::kStages + s); };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
-  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
-  int* offs = reinterpret_cast<int*>(smem + C::kOffsOff);
+  int* offs = reinterpret_cast<int*>(smem + kOffsOff);
   int* prefix = offs + 260;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kBlk = block_bytes(kStepK / GP);
 
-  if (threadIdx.x == 32) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), kWarps);
-    }
-    *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    fence_async_smem();
-  }
   if (warp == 0) load_segments(a.offsets, a.E, a.rows_cap, kRows, 1, offs, prefix, a.status, blockIdx.x == 0);
   __syncthreads();
 
-  const Q4Shape q(a.K, a.N, kStepK / GP);
-  const int strips = (q.tiles + kWarps - 1) / kWarps;
-  const long long total = (long long)prefix[a.E] * strips * q.steps;
-  const long long ctas = min((long long)gridDim.x, total);  // every CTA up to here has a step at least
-  const int c = blockIdx.x;
-  const long long u0 = c < ctas ? total * c / ctas : 0, u1 = c < ctas ? total * (c + 1) / ctas : 0;
-
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ producer ---------------------
-    int stage = 0;
-    uint32_t phase = 0;
-    int armed[C::kStages];
+  // this CTA's pieces [p0, p0 + n), and the number of warps that share one: the rounds that n pieces take with 16 / S
+  // teams, each of ceil(steps / S) steps and, with S > 1, about two more for joining the sums
+  const int total = prefix[a.E] * a.pairs;
+  const int base = idiv(total, gridDim.x), extra = total - base * gridDim.x;
+  const int p0 = blockIdx.x * base + min((int)blockIdx.x, extra), n = base + ((int)blockIdx.x < extra);
+  int ls = 0, best = 0x7fffffff;
 #pragma unroll
-    for (int s = 0; s < C::kStages; ++s) armed[s] = -1;
-    bool ok = true;
-    constexpr int ES = F32X ? 4 : 2;
-    for (long long u = u0; u < u1 && ok;) {
-      const long long item = u / q.steps;
-      const int k_first = (int)(u - item * q.steps);
-      const int k_last = (int)min((long long)q.steps, k_first + (u1 - u));
-      const Q4Item it = find_item(item, offs, prefix, a.E, strips);
-      const int nt = q.strip_tiles(it.strip);
-      const uint8_t* w = a.w + (size_t)it.e * q.expert_bytes();
-      const uint8_t* xrow = a.x + ((size_t)it.row0 + lane) * a.ldx * ES;
-      for (int k = k_first; k < k_last; ++k) {
-        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, a.wait_limit, abort_flag, a.status,
-                                               kDevTimeoutProducer))) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = sbase + stage * C::kStageBytes;
-        const uint32_t wbytes = (uint32_t)(nt * q.blk), xbytes = (uint32_t)(min(kStepK, a.K - k * kStepK) * ES);
-        if (lane == 0) {
-          mbar_arrive_expect_tx(full_bar(stage), wbytes + (uint32_t)it.rows * xbytes);
-          bulk_load(dst, w + q.at(it.strip, k), wbytes, full_bar(stage));
-        }
-        __syncwarp();
-        if (lane < it.rows)
-          bulk_load(dst + C::kWBytes + lane * (F32X ? kStepK * 4 : kXPitch), xrow + (size_t)k * kStepK * ES, xbytes,
-                    full_bar(stage));
-#pragma unroll
-        for (int s = 0; s < C::kStages; ++s)
-          if (s == stage) armed[s] = (int)phase;
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      u += k_last - k_first;
+  for (int l = 0; l <= 4; ++l) {
+    const int cost = ((n + (16 >> l) - 1) >> (4 - l)) * (((a.steps + (1 << l) - 1) >> l) + (l ? 2 : 0));
+    if (cost < best) {
+      best = cost;
+      ls = l;
     }
-    if (!ok || *abort_flag) {
-      // every armed stage's copies must land before the CTA exits
-#pragma unroll
-      for (int s = 0; s < C::kStages; ++s)
-        if (armed[s] >= 0) {
-          volatile int dummy = 0;
-          mbar_wait(full_bar(s), (uint32_t)armed[s], a.wait_limit, &dummy, a.status, kDevTimeoutDrain);
-        }
-    }
-    return;
   }
+  const int team = warp >> ls, slice = warp & ((1 << ls) - 1), teams = kWarps >> ls;
+  const int k0 = (slice * a.steps) >> ls, k1 = ((slice + 1) * a.steps) >> ls;
 
-  // -------------------------------------------------------------- consumers --------------------
-  const int g = lane >> 2, t = lane & 3;
-  int stage = 0, plane = 0;
-  uint32_t phase = 0;
-  bool ok = true;  // after a wait that ran out the loops go on without work, so that the barriers below still match
-  for (long long u = u0; u < u1;) {
-    const long long item = u / q.steps;
-    const int k_first = (int)(u - item * q.steps);
-    const int k_last = (int)min((long long)q.steps, k_first + (u1 - u));
-    const Q4Item it = find_item(item, offs, prefix, a.E, strips);
-    const int nt = q.strip_tiles(it.strip);
-    const bool mine = warp < nt;
-    const int nrb = (it.rows + 7) / 8;
-    float acc[kRows / 8][4] = {};
-    for (int k = k_first; k < k_last; ++k) {
-      if (ok) ok = mbar_wait(full_bar(stage), phase, a.wait_limit, abort_flag, a.status, kDevTimeoutMma);
-      ok = __all_sync(0xffffffffu, ok);
-      const uint32_t st = sbase + stage * C::kStageBytes;
-      const int kk = min(kStepK, a.K - k * kStepK);
-      uint32_t xs = st + C::kWBytes;
-      if constexpr (F32X) {
-        // eight inputs of one row a thread: raw fp32 into three planes of bf16
-        const uint32_t raw = xs;
-        xs = sbase + C::kPlaneOff + plane * (3 * kRows * kXPitch);
-        const int row = threadIdx.x >> 4, seg = threadIdx.x & 15;
-        if (ok && row < it.rows && seg * 8 < kk) {
-          const uint4 v0 = lds128(raw + row * (kStepK * 4) + seg * 32), v1 = lds128(raw + row * (kStepK * 4) + seg * 32 + 16);
-          const uint32_t v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-          uint32_t p[3][4];
+  const uint32_t ring = sbase + warp * (kStages * kStageBytes);
+  float4* swap = reinterpret_cast<float4*>(smem + kSwapOff);
+  const Unpack unpack;
+  for (int i = team; i < n; i += teams) {
+    const Q4Piece p = find_piece(p0 + i, offs, prefix, a.E, a.pairs);
+    const uint8_t* first = a.w + (((size_t)p.e * a.pairs + p.pair) * a.steps + k0) * kBlk;
+    float acc[2][2][4] = {};  // tile, group of 8 rows
+    if (p.rows <= 8) q4_run<GP, F32X, 1>(a, p, k0, k1, first, ring, lane, unpack, acc);
+    else q4_run<GP, F32X, 2>(a, p, k0, k1, first, ring, lane, unpack, acc);
+    if (ls > 0) {
+      if (i >= teams) team_sync(team, 1 << ls);  // the swap space has been read
+      if (slice > 0) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t lo[3], hi[3];
-            split3(__uint_as_float(v[2 * j]), lo[0], lo[1], lo[2]);
-            split3(__uint_as_float(v[2 * j + 1]), hi[0], hi[1], hi[2]);
-#pragma unroll
-            for (int i = 0; i < 3; ++i) p[i][j] = __byte_perm(lo[i], hi[i], 0x7632);
-          }
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            sts128(xs + i * kRows * kXPitch + row * kXPitch + seg * 16, p[i][0], p[i][1], p[i][2], p[i][3]);
-        }
-        plane ^= 1;  // the other planes are free: every warp has passed the barrier behind their last use
-        ok = consumers_all(ok);
+        for (int q = 0; q < 4; ++q)
+          if (q < 2 || p.rows > 8)
+            swap[(warp * 4 + q) * 32 + lane] = make_float4(acc[q & 1][q >> 1][0], acc[q & 1][q >> 1][1], acc[q & 1][q >> 1][2], acc[q & 1][q >> 1][3]);
       }
-      if (ok && mine) {
-        const uint32_t wblk = st + warp * q.blk;
-        constexpr int P = F32X ? 3 : 1;
-        if (nrb == 1) q4_step<GP, P, 1>(acc, wblk, xs, kk / 32, lane);
-        else if (nrb == 2) q4_step<GP, P, 2>(acc, wblk, xs, kk / 32, lane);
-        else q4_step<GP, P, 4>(acc, wblk, xs, kk / 32, lane);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty_bar(stage));
-      if (++stage == C::kStages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
-    u += k_last - k_first;
-
-    bool write = ok;
-    if (k_last - k_first < q.steps) {
-      // part of the item's sum: leave it, and let the last of its CTAs add all parts
-      const long long f = item * q.steps;
-      const int c0 = (int)(((f + 1) * ctas - 1) / total), c1 = (int)(((f + q.steps) * ctas - 1) / total);
-      auto slot = [&](int cta) {  // a CTA's first item may have begun before it, its last one end after it
-        return a.partials + ((size_t)cta * 2 + (cta > c0 ? 0 : 1)) * (kPartialBytes / 16) + (size_t)warp * (kRows / 8) * 32 + lane;
-      };
-      if (mine) {
-        float4* dst = slot(c);
+      team_sync(team, 1 << ls);
+      if (slice > 0) continue;
+      for (int o = 1; o < 1 << ls; ++o) {
 #pragma unroll
-        for (int rb = 0; rb < kRows / 8; ++rb)
-          if (rb < nrb) __stcg(dst + rb * 32, make_float4(acc[rb][0], acc[rb][1], acc[rb][2], acc[rb][3]));
-      }
-      __threadfence();
-      write = consumers_all(ok);
-      if (threadIdx.x == 0) {
-        int last = 0;
-        if (write) {
-          last = atomicAdd(a.counters + c0, 1u) == (unsigned)(c1 - c0);
-          if (last) a.counters[c0] = 0;  // for the next call
-        }
-        *last_flag = last;
-        __threadfence();
-      }
-      consumers_all(true);
-      write = *last_flag != 0;
-      if (write && mine) {
-#pragma unroll
-        for (int rb = 0; rb < kRows / 8; ++rb) acc[rb][0] = acc[rb][1] = acc[rb][2] = acc[rb][3] = 0.f;
-        for (int o = c0; o <= c1; o += 4) {
-          float4 v[4][kRows / 8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int rb = 0; rb < kRows / 8; ++rb)
-              v[j][rb] = o + j <= c1 && rb < nrb ? __ldcg(slot(o + j) + rb * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int rb = 0; rb < kRows / 8; ++rb) {
-              acc[rb][0] += v[j][rb].x;
-              acc[rb][1] += v[j][rb].y;
-              acc[rb][2] += v[j][rb].z;
-              acc[rb][3] += v[j][rb].w;
-            }
+        for (int q = 0; q < 4; ++q) {
+          if (q >= 2 && p.rows <= 8) continue;
+          const float4 v = swap[((warp + o) * 4 + q) * 32 + lane];
+          acc[q & 1][q >> 1][0] += v.x;
+          acc[q & 1][q >> 1][1] += v.y;
+          acc[q & 1][q >> 1][2] += v.z;
+          acc[q & 1][q >> 1][3] += v.w;
         }
       }
     }
-    if (write && mine) {
-      // lane: columns n and n + 8, rows 2t and 2t + 1 of each group of 8
-      const int n0 = it.strip * (16 * kWarps) + warp * 16 + g;
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      const int m = q & 1, rb = q >> 1;
+      if (rb * 8 >= p.rows) continue;
+      float sum[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + (j >> 1) * 8;
-        if (n >= a.N) continue;
-        float b = 0.f;
-        if (a.bias != nullptr)
-          b = F32X ? static_cast<const float*>(a.bias)[(size_t)it.e * a.N + n]
-                   : __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[(size_t)it.e * a.N + n]);
+      for (int j = 0; j < 4; ++j) sum[j] = rb ? (m ? acc[1][1][j] : acc[0][1][j]) : (m ? acc[1][0][j] : acc[0][0][j]);
+      const int row0 = p.row0 + rb * 8, rows = p.rows - rb * 8, n0 = p.pair * 32 + m * 16;
+      if constexpr (!F32X) {
+        bool finite = true;
 #pragma unroll
-        for (int rb = 0; rb < kRows / 8; ++rb) {
-          const int r = rb * 8 + 2 * t + (j & 1);
-          if (r >= it.rows) continue;
-          float v = acc[rb][j] + b;
-          const size_t at = ((size_t)it.row0 + r) * a.ldy + n;
-          if (a.bf16_out) {
-            if (a.act == MOE_ACT_GELU) v = activate<MOE_ACT_GELU, true>(v);
-            else if (a.act == MOE_ACT_SILU) v = activate<MOE_ACT_SILU, true>(v);
-            static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
-          } else {
-            if (a.act == MOE_ACT_GELU) v = activate<MOE_ACT_GELU, false>(v);
-            else if (a.act == MOE_ACT_SILU) v = activate<MOE_ACT_SILU, false>(v);
-            static_cast<float*>(a.y)[at] = v;
-          }
+        for (int j = 0; j < 4; ++j) finite = finite && (2 * t + (j & 1) >= rows || fabsf(sum[j]) < INFINITY);
+        if (__any_sync(0xffffffffu, !finite)) {
+          const float4 again = sums_term_by_term(a, a.w + (size_t)p.e * a.pairs * a.steps * kBlk, kStepK / GP, n0, row0, rows, lane);
+          const float v[4] = {again.x, again.y, again.z, again.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)  // a row's result does not depend on its neighbours: the others keep their sums
+            if (!(fabsf(sum[j]) < INFINITY)) sum[j] = v[j];
         }
       }
+      store_unit<F32X>(a, p.e, n0 + g, row0 + 2 * t, rows - 2 * t, sum);
     }
   }
 }
@@ -432,20 +463,21 @@ __global__ void __launch_bounds__(kThreadsQ4, 1) q4_matmul_kernel(Q4Args a) {
 // ---------------------------------------------------------------- laying the weights out --------
 // One thread a lane's 16 bytes of a tile's 64 inputs: word 2h + i holds inputs 32h + 8t + 4i + {0..3} of columns
 // g and g + 8, its 16-bit halves the even and the odd ones, each with (g, first), (g + 8, first), (g, second),
-// (g + 8, second).  Columns and inputs past the edge are code 8 (zero) with scale zero.
+// (g + 8, second), the word turned left by 3: code j sits at bits 3 + 4 j of its half, where a turn right by 4 j and a
+// mask leave it in the mantissa of 16 + c.  Columns and inputs past the edge are code 8 (zero) with scale zero.
 __global__ void __launch_bounds__(256) q4_pack_kernel(int E, int K, int N, int group, const uint8_t* __restrict__ q,
                                                       const uint16_t* __restrict__ s, uint8_t* __restrict__ packed) {
   const Q4Shape sh(K, N, group);
-  const long long units = (long long)E * sh.tiles * sh.steps * 2;
+  const int tiles = 2 * sh.pairs;
+  const long long units = (long long)E * tiles * sh.steps * 2;
   const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (i >= units) return;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int u = (int)(i & 1);
   const long long b = i >> 1;
   const int step = (int)(b % sh.steps);
-  const int tile = (int)((b / sh.steps) % sh.tiles), e = (int)(b / sh.steps / sh.tiles);
-  const int strip = tile / kWarps;
-  uint8_t* dst = packed + (size_t)e * sh.expert_bytes() + sh.at(strip, step) + (size_t)(tile - strip * kWarps) * sh.blk;
+  const int tile = (int)((b / sh.steps) % tiles), e = (int)(b / sh.steps / tiles);
+  uint8_t* dst = packed + (size_t)e * sh.expert_bytes() + sh.at(tile >> 1, step);
   uint32_t w[4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -465,10 +497,10 @@ __global__ void __launch_bounds__(256) q4_pack_kernel(int E, int K, int N, int g
         for (int f = 0; f < 2; ++f)
 #pragma unroll
           for (int j = 0; j < 2; ++j) r |= ((v[j] >> (16 * p + 8 * f + 4 * o)) & 15u) << (16 * o + 8 * f + 4 * j);
-      w[2 * h + p] = r;
+      w[2 * h + p] = r << 3 | r >> 29;
     }
   }
-  *reinterpret_cast<uint4*>(dst + u * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(dst + (tile & 1) * 1024 + u * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   const int gp = kStepK / group;
   if (u == 0 && lane < gp * 8) {
     const int grp = lane >> 3, kg = step * gp + grp, groups = K / group;
@@ -478,20 +510,8 @@ __global__ void __launch_bounds__(256) q4_pack_kernel(int E, int K, int N, int g
       const int n = tile * 16 + (lane & 7) + 8 * j;
       if (n < N && kg < groups) v |= (uint32_t)s[((size_t)e * groups + kg) * N + n] << (16 * j);
     }
-    *reinterpret_cast<uint32_t*>(dst + 1024 + lane * 4) = v;
+    *reinterpret_cast<uint32_t*>(dst + 2048 + (tile & 1) * gp * 32 + lane * 4) = v;
   }
-}
-
-// The value of one weight in the packed layout
-__device__ __forceinline__ float q4_value(const uint8_t* expert, const Q4Shape& sh, int group, int k, int n) {
-  const int tile = n >> 4, strip = tile / kWarps, step = k / kStepK, r = k % kStepK;
-  const uint8_t* blk = expert + sh.at(strip, step) + (size_t)(tile - strip * kWarps) * sh.blk;
-  const int lane = (n & 7) * 4 + ((r & 31) >> 3);
-  const int word = ((r & 63) >> 5) * 2 + ((r & 7) >> 2), field = ((r & 3) >> 1) * 2 + ((n >> 3) & 1);
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + (r >> 6) * 512 + lane * 16 + word * 4);
-  const int code = (int)((w >> (16 * (r & 1) + 4 * field)) & 15u);
-  const uint32_t sc = *reinterpret_cast<const uint32_t*>(blk + 1024 + (r / group) * 32 + (n & 7) * 4);
-  return (float)(code - 8) * __uint_as_float((n & 8) ? sc & 0xffff0000u : sc << 16);  // 4 by 8 bits: exact
 }
 
 template <typename T>
@@ -554,6 +574,11 @@ moe_status_t check_q4(int64_t E, int64_t K, int64_t N, int group) {
   return MOE_OK;
 }
 
+// Pieces of a call at most: its rows in blocks of 16, one ragged block an expert
+long long most_pieces(const moe_q4_t& m) {
+  return (m.rows_cap / kRows + (m.rows_cap < m.E ? m.rows_cap : m.E)) * (((long long)m.N + 31) / 32);
+}
+
 unsigned copy_grid(long long threads) {
   const long long blocks = (threads + 255) / 256;
   return (unsigned)(blocks < 1 << 20 ? blocks : 1 << 20);
@@ -561,9 +586,9 @@ unsigned copy_grid(long long threads) {
 
 template <int GP, bool F32X>
 cudaError_t launch_q4(const Q4Args& a, int grid, cudaStream_t st) {
-  const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(q4_matmul_kernel<GP, F32X>), Q4Cfg<F32X>::kSmemBytes);
+  const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(q4_matmul_kernel<GP, F32X>), kSmemBytes);
   if (err != cudaSuccess) return err;
-  q4_matmul_kernel<GP, F32X><<<grid, kThreadsQ4, Q4Cfg<F32X>::kSmemBytes, st>>>(a);
+  q4_matmul_kernel<GP, F32X><<<grid, 32 * kWarps, kSmemBytes, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -582,15 +607,15 @@ moe_status_t check_q4_matmul(const moe_q4_t* m, const void* ws, size_t ws_bytes)
   if (st != MOE_OK) return st;
   if (m->dtype == MOE_DTYPE_F32 && m->out_dtype != MOE_DTYPE_F32) return MOE_ERR_UNSUPPORTED;
   if (ldx % (m->dtype == MOE_DTYPE_BF16 ? 8 : 4) != 0 || m->rows_cap >= (1LL << 31) - 1024) return MOE_ERR_UNSUPPORTED;
-  if (ldx >= (1LL << 31) || ldy >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+  if (ldx >= (1LL << 31) || ldy >= (1LL << 31) || most_pieces(*m) >= 1LL << 31) return MOE_ERR_UNSUPPORTED;
   if (ws == nullptr || misaligned(ws, 256)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < kQ4WsBytes) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
 
-// m, ws and the pointers have been checked; status may be another workspace's error word
+// m and the pointers have been checked
 cudaError_t launch_q4_matmul(const moe_q4_t& m, const int32_t* offsets, const void* x, const void* packed, const void* bias,
-                             void* y, void* ws, int32_t* status, cudaStream_t st) {
+                             void* y, int32_t* status, cudaStream_t st) {
   Q4Args a{};
   a.offsets = offsets;
   a.x = static_cast<const uint8_t*>(x);
@@ -598,8 +623,6 @@ cudaError_t launch_q4_matmul(const moe_q4_t& m, const int32_t* offsets, const vo
   a.bias = bias;
   a.y = y;
   a.status = status;
-  a.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + kCounterOff);
-  a.partials = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + kPartialOff);
   a.rows_cap = m.rows_cap;
   a.ldx = m.ldx == 0 ? m.K : m.ldx;
   a.ldy = m.ldy == 0 ? m.N : m.ldy;
@@ -608,12 +631,11 @@ cudaError_t launch_q4_matmul(const moe_q4_t& m, const int32_t* offsets, const vo
   a.N = m.N;
   a.act = m.activation;
   a.bf16_out = m.out_dtype == MOE_DTYPE_BF16;
-  a.wait_limit = wait_limit();
   const Q4Shape q(m.K, m.N, m.group);
-  const long long most = (m.rows_cap / kRows + (m.rows_cap < m.E ? m.rows_cap : m.E)) * ((q.tiles + kWarps - 1) / kWarps) * q.steps;
-  int grid = sm_count();
-  if (grid > kMaxCtas) grid = kMaxCtas;
-  if (grid > most) grid = (int)most;
+  a.steps = q.steps;
+  a.pairs = q.pairs;
+  const long long pieces = most_pieces(m);
+  const int grid = pieces < sm_count() ? (int)pieces : sm_count();
   const bool f32 = m.dtype == MOE_DTYPE_F32;
   if (m.group == 32) return f32 ? launch_q4<4, true>(a, grid, st) : launch_q4<4, false>(a, grid, st);
   if (m.group == 64) return f32 ? launch_q4<2, true>(a, grid, st) : launch_q4<2, false>(a, grid, st);
@@ -643,7 +665,7 @@ moe_status_t moe_q4_pack(int32_t E, int32_t K, int32_t N, int32_t group, const v
       misaligned(packed, 16))
     return MOE_ERR_INVALID_ARG;
   const Q4Shape q(K, N, group);
-  const long long blocks = ((long long)E * q.tiles * q.steps * 2 + 7) / 8;
+  const long long blocks = ((long long)E * q.pairs * q.steps * 4 + 7) / 8;
   if (blocks >= 1LL << 31) return MOE_ERR_UNSUPPORTED;
   q4_pack_kernel<<<(unsigned)blocks, 256, 0, stream>>>(E, K, N, group, static_cast<const uint8_t*>(codes),
                                                        static_cast<const uint16_t*>(scales), static_cast<uint8_t*>(packed));
@@ -704,7 +726,7 @@ moe_status_t moe_q4_matmul(const moe_q4_t* m, const int32_t* offsets, const void
   if (offsets == nullptr || x == nullptr || packed == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
   if (misaligned(offsets, 4) || misaligned(x, 16) || misaligned(packed, 16) || misaligned(bias, es) || misaligned(y, os))
     return MOE_ERR_INVALID_ARG;
-  if (launch_q4_matmul(*m, offsets, x, packed, bias, y, ws, static_cast<int32_t*>(ws), stream) != cudaSuccess)
+  if (launch_q4_matmul(*m, offsets, x, packed, bias, y, static_cast<int32_t*>(ws), stream) != cudaSuccess)
     return MOE_ERR_CUDA;
   ++launch_count();
   return MOE_OK;

@@ -129,7 +129,6 @@ def check(counts, K, N, group, dtype=BF, out_dtype=None, act=None, bias=True, pa
     assert y.data_ptr() == out.data_ptr()
     within(y[:n], ref[:n], bound[:n] + round_bound(ref[:n].abs() + bound[:n], out_dtype), f"{counts} {K} {N} {group}")
     assert (buf[n:] == 7.0).all() and (buf[:, N:] == 7.0).all(), "wrote outside its rows or columns"
-    assert not ws[256:4096].any(), "counters left behind"
 
 
 ROWS = [[1], [0, 1, 0], [8, 0, 9, 1], [16, 17, 24, 25], [31, 32, 33], [0, 100, 7], [65]]

@@ -201,8 +201,8 @@ def test_q4_pointers_and_workspace():
 
 
 def test_q4_layout_calls():
-    assert moe.moe_q4_packed_size(2, 128, 16, 64) == 2 * (1024 + 64)
-    assert moe.moe_q4_packed_size(1, 160, 17, 32) == 2 * 2 * (1024 + 128)  # two steps of 128, two tiles of 16
+    assert moe.moe_q4_packed_size(2, 128, 16, 64) == 2 * 2 * (1024 + 64)  # 32 columns a block
+    assert moe.moe_q4_packed_size(1, 160, 33, 32) == 2 * 2 * 2 * (1024 + 128)  # two steps of 128, two blocks of 32
     for E, K, N, group, code in ((0, 128, 8, 64, 1), (1, 128, 8, 48, 1), (1, 0, 8, 64, 1), (1, 128, 0, 64, 1), (1, 96, 8, 64, 2)):
         assert moe.moe_q4_packed_size(E, K, N, group) == 0
         assert moe.moe_q4_pack(E, K, N, group, FAKE, FAKE, FAKE) == code
