@@ -521,16 +521,14 @@ typedef struct {
 
 /* y[r,n] = act(sum_k x[r,k] * W[e,k,n] + bias[e,n]) for every row r of expert e, W in the packed layout.  Rows,
  * offsets (clamped on the device, and recorded) and what is left unwritten are as in moe_grouped_matmul.
- * ws: a device buffer of moe_q4_workspace_size() bytes, 256-byte aligned, zero before its first use; calls on
- * one workspace have to follow each other (one stream, or events between), also as graphs that captured it;
- * calls on workspaces of their own may run at once.  Its first word is the error word for moe_get_device_status;
- * after a timeout there, zero the workspace again.  Sums run in a fixed order: the same call gives the same bits
- * on the same GPU.  Any number of rows is computed; the kernel is made for a few (up to 32 an expert read the
- * weights once).  Errors: MOE_ERR_INVALID_ARG (sizes and pointers as above; rows_cap < 0; a pitch below the row;
+ * ws: a device buffer of moe_q4_workspace_size() bytes, 256-byte aligned, zero before its first use.  It holds
+ * the error word for moe_get_device_status alone, so any number of calls may share one.  Sums run in a fixed order:
+ * the same call gives the same bits on the same GPU.  Any number of rows is computed; the kernel is made for a few
+ * (the weights are read once for every 16 rows of an expert).  Errors: MOE_ERR_INVALID_ARG (sizes and pointers as above; rows_cap < 0; a pitch below the row;
  * an unknown type or activation; x not 16-byte aligned, y, bias and offsets below their type's alignment; ws null
  * or misaligned), MOE_ERR_UNSUPPORTED (K not a multiple of group, ldx as above, fp32 x with a bf16 y, K or N above
- * 2^24, a pitch of 2^31 or more, rows_cap >= 2^31 - 1024, more than 2^31 pieces of 32 rows, 256 columns and 128
- * inputs), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.  1 launch; none for rows_cap = 0. */
+ * 2^24, a pitch of 2^31 or more, rows_cap >= 2^31 - 1024, more than 2^31 pieces of 16 rows and 32 columns),
+ * MOE_ERR_WORKSPACE, MOE_ERR_CUDA.  1 launch; none for rows_cap = 0. */
 MOE_API size_t moe_q4_workspace_size(void);
 MOE_API moe_status_t moe_q4_matmul(const moe_q4_t* m, const int32_t* offsets, const void* x, const void* packed,
                                    const void* bias, void* y, void* ws, size_t ws_bytes, cudaStream_t stream);
@@ -539,11 +537,9 @@ MOE_API moe_status_t moe_q4_matmul(const moe_q4_t* m, const int32_t* offsets, co
  * reading W1q (K = H, N = F) and W2q (K = F, N = H) in place of io->W1 and io->W2 (which may be null).  h is kept
  * in the storage type and y in fp32, in the layer's workspace; combine = 1 also runs moe_combine's sum into
  * io->out, 0 leaves y for a later moe_combine.  shape, io, ws and their errors as moe_expert_ffn; group must divide
- * H and F (MOE_ERR_UNSUPPORTED).  q4_ws: as ws of moe_q4_matmul; errors on the device are recorded in ws.
- * 2 launches, 3 with combine. */
+ * H and F (MOE_ERR_UNSUPPORTED).  2 launches, 3 with combine. */
 MOE_API moe_status_t moe_expert_ffn_q4(const moe_shape_t* shape, const moe_io_t* io, int32_t group, const void* W1q,
-                                       const void* W2q, void* ws, size_t ws_bytes, void* q4_ws, size_t q4_ws_bytes,
-                                       int combine, cudaStream_t stream);
+                                       const void* W2q, void* ws, size_t ws_bytes, int combine, cudaStream_t stream);
 
 /* Kernel-selection switches for side-by-side comparisons of the kernels; normal use needs none.
  *   MOE_KERNEL_NO_CTA_PAIR  single-CTA 128-row grouped-GEMM tiles everywhere, instead of the CTA-pair

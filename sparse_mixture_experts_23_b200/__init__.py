@@ -164,7 +164,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_q4_workspace_size.restype = sz
     lib.moe_q4_matmul.argtypes = [P(Q4), vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_q4_matmul.restype = st
-    lib.moe_expert_ffn_q4.argtypes = [P(Shape), P(IO), i32, vp, vp, vp, sz, vp, sz, ctypes.c_int, vp]
+    lib.moe_expert_ffn_q4.argtypes = [P(Shape), P(IO), i32, vp, vp, vp, sz, ctypes.c_int, vp]
     lib.moe_expert_ffn_q4.restype = st
     lib.moe_debug_activation.argtypes = [ctypes.c_int, vp, vp, ctypes.c_int64, vp]
     lib.moe_debug_activation.restype = st
@@ -355,9 +355,9 @@ def moe_q4_matmul(m: Q4, offsets, x, packed, bias, y, ws, ws_bytes, stream=0) ->
     return load_library().moe_q4_matmul(ctypes.byref(m), offsets, x, packed, bias, y, ws, ws_bytes, stream)
 
 
-def moe_expert_ffn_q4(shape, io, group, W1q, W2q, ws, ws_bytes, q4_ws, q4_ws_bytes, combine=1, stream=0) -> int:
-    return load_library().moe_expert_ffn_q4(ctypes.byref(shape), ctypes.byref(io), group, W1q, W2q, ws, ws_bytes, q4_ws,
-                                            q4_ws_bytes, int(combine), stream)
+def moe_expert_ffn_q4(shape, io, group, W1q, W2q, ws, ws_bytes, combine=1, stream=0) -> int:
+    return load_library().moe_expert_ffn_q4(ctypes.byref(shape), ctypes.byref(io), group, W1q, W2q, ws, ws_bytes,
+                                            int(combine), stream)
 
 
 def moe_debug_activation(activation: int, u, out, n: int, stream=0) -> int:
@@ -441,24 +441,21 @@ class MoEBuffers:
         return _check(moe_expert_ffn(self.shape, self.io, self.ws_ptr, self.ws_bytes, int(fuse_combine), self.stream()),
                       "moe_expert_ffn")
 
-    def expert_ffn_q4(self, W1, W2, q4_ws, combine=True):
-        """expert_ffn with 4-bit weights: W1 and W2 are ``Q4Weights`` of one group size (W1 H by F, W2 F by H),
-        q4_ws a ``q4_workspace()``.  The layer's biases and activation apply; inputs W1 and W2 are not read."""
+    def expert_ffn_q4(self, W1, W2, combine=True):
+        """expert_ffn with 4-bit weights: W1 and W2 are ``Q4Weights`` of one group size (W1 H by F, W2 F by H).
+        The layer's biases and activation apply; inputs W1 and W2 are not read."""
         s = self.shape
         for name, w, K, N in (("W1", W1, s.H, s.F), ("W2", W2, s.F, s.H)):
             if (w.E, w.K, w.N) != (s.E, K, N) or w.group != W1.group or w.packed.device != self.ws.device:
                 raise ValueError(f"{name} must hold [{s.E}, {K}, {N}] in groups of {W1.group} on {self.ws.device}")
-        if q4_ws.device != self.ws.device:
-            raise ValueError(f"q4_ws must be on {self.ws.device}")
         return _check(moe_expert_ffn_q4(s, self.io, W1.group, W1.packed.data_ptr(), W2.packed.data_ptr(), self.ws_ptr,
-                                        self.ws_bytes, q4_ws.data_ptr(), q4_ws.numel() * q4_ws.element_size(), int(combine),
-                                        self.stream()), "moe_expert_ffn_q4")
+                                        self.ws_bytes, int(combine), self.stream()), "moe_expert_ffn_q4")
 
-    def forward_q4(self, W1, W2, q4_ws):
+    def forward_q4(self, W1, W2):
         """The layer's forward pass with its experts in 4 bits: route, permute, expert_ffn_q4 with the combine."""
         self.route()
         self.permute()
-        return self.expert_ffn_q4(W1, W2, q4_ws)
+        return self.expert_ffn_q4(W1, W2)
 
     def combine(self):
         return _check(moe_combine(self.shape, self.io, self.ws_ptr, self.ws_bytes, self.stream()), "moe_combine")

@@ -522,8 +522,7 @@ moe_status_t moe_expert_ffn(const moe_shape_t* shape, const moe_io_t* io, void* 
 }
 
 moe_status_t moe_expert_ffn_q4(const moe_shape_t* shape, const moe_io_t* io, int32_t group, const void* W1q,
-                               const void* W2q, void* ws, size_t ws_bytes, void* q4_ws, size_t q4_ws_bytes, int combine,
-                               cudaStream_t stream) {
+                               const void* W2q, void* ws, size_t ws_bytes, int combine, cudaStream_t stream) {
   NvtxRange nvtx_range("moe_expert_ffn_q4");
   g_launches = 0;
   moe_status_t st = check_shape(shape);
@@ -539,13 +538,13 @@ moe_status_t moe_expert_ffn_q4(const moe_shape_t* shape, const moe_io_t* io, int
   m.group = group;
   m.dtype = m.out_dtype = shape->dtype;
   m.activation = shape->activation;
-  if ((st = check_q4_matmul(&m, q4_ws, q4_ws_bytes)) != MOE_OK) return st;
+  if ((st = check_q4_matmul(&m)) != MOE_OK) return st;
   moe_q4_t m2 = m;
   m2.K = shape->F;
   m2.N = shape->H;
   m2.out_dtype = MOE_DTYPE_F32;
   m2.activation = MOE_ACT_NONE;
-  if ((st = check_q4_matmul(&m2, q4_ws, q4_ws_bytes)) != MOE_OK) return st;
+  if ((st = check_q4_matmul(&m2)) != MOE_OK) return st;
   const bool ec = shape->routing == MOE_ROUTING_EXPERT_CHOICE;
   if (shape->T == 0) return MOE_OK;
   if (null_any({W1q, W2q, io->topk_w}) || (combine && (io->out == nullptr || (ec && io->topk_idx == nullptr))))

@@ -343,9 +343,9 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedArgs& a, cudaStream_t st);
 cudaError_t launch_grouped_wgrad_sm100(const GroupedArgs& a, const void* dy, float* dW, cudaStream_t st);
 
 // ---- products with 4-bit weights (moe_q4_matmul, moe_expert_ffn_q4) ----
-// Argument rules of sizes, types and the workspace.
-moe_status_t check_q4_matmul(const moe_q4_t* m, const void* ws, size_t ws_bytes);
-// Arguments that have passed them, rows_cap > 0.  1 launch.
+// Argument rules of sizes and types.
+moe_status_t check_q4_matmul(const moe_q4_t* m);
+// Arguments that have passed them, rows_cap > 0; status: the error word.  1 launch.
 cudaError_t launch_q4_matmul(const moe_q4_t& m, const int32_t* offsets, const void* x, const void* packed, const void* bias,
                              void* y, int32_t* status, cudaStream_t st);
 

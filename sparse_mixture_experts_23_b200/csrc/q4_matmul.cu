@@ -5,14 +5,12 @@
 //
 // Bound: reading the weights from HBM (half a byte each), as decode with bf16 weights is by four times the bytes.
 // Mathematics: a sum over up to 64 inputs of a group,  d[n,r] = sum_k (c - 8) x[r,k],  runs on mma.sync m16n8k16 with
-// the weights as the 16-row operand and eight rows of x as the 8-column one, and joins the fp32 accumulator as
-// acc += s d:  no weight is rounded, and tensor-core sums (which cut) are short.  Unpacking sets the pace next to the
-// bytes: one shift and one logic instruction make 16 + c of two codes.  The -24 is not taken from every weight but
-// once for a warp's 32 columns, d = sum (-24) x + sum (16 + c) x, the first sum being one more product with a constant
-// operand that the second starts from; what cancels is five times the result's size, so about 2^-21 of the summed
-// magnitudes are lost.  An infinity in x (or an overflow of the larger terms) would leave NaN there: a sum that is not
-// finite is computed again term by term.  For fp32 rows 24 is subtracted from each unpacked weight (exact in bf16),
-// and the rows are split exactly into three bf16 parts (8 bits of the significand each), three products a step.
+// the weights as the 16-row operand (c - 8 is exact in bf16) and eight rows of x as the 8-column one, and joins the
+// fp32 accumulator as  acc += s d:  no weight is rounded, and tensor-core sums (which cut) are short.  fp32 rows are
+// split exactly into three bf16 parts (8 bits of the significand each), three products a step.
+// Unpacking sets the pace next to the bytes: a turn of the word and one logic instruction make 16 + c of two codes, a
+// subtraction c - 8.  (Taking 24 sum x from the result instead, by one more product with a constant operand for both
+// tiles, measured no faster: the tensor pipe's clocks cost what the subtractions do.)
 // mma.sync rather than tcgen05: at up to 16 rows the product is a small part of what the tensor pipe could do in the
 // time that the weights take, and its register operand is what unpacking produces.
 //
@@ -22,8 +20,9 @@
 // Split: a piece of work is two tiles of an expert's block of up to 16 rows, over all of K.  The pieces are shared over
 // one CTA per SM, and its 16 warps work alone: each streams its piece's blocks through a ring of its own (16-byte
 // asynchronous copies, 9 KB in flight a warp, each lane the codes that it will read itself) and reads x through L1,
-// once for its two tiles.  Where a CTA has fewer pieces than warps (or an uneven number), 2 to 16 warps share a piece's
-// steps and add their sums in shared memory, in order.  Nothing crosses a CTA: with K split over CTAs, joining parts
+// once for its two tiles.  The steps of a CTA's pieces laid end to end are shared evenly over its warps (two rounds of
+// whole pieces cost the layer of many experts 1.6 times as much); where a piece is cut, the warp that has its beginning
+// adds the others' sums from shared memory, in order.  Nothing crosses a CTA: with K split over CTAs, joining parts
 // through global memory took 4 to 5 us each of a call that streams for 10; with stages and x shared by a CTA's warps,
 // the waits for one another and a fragment of x for every tile took as long as the bytes; and bulk copies of 1 KB are
 // too slow: an SM issues one in about 64 clocks.
@@ -88,10 +87,6 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(a));
   return v;
 }
-// the warps of a team meet
-__device__ __forceinline__ void team_sync(int team, int warps) {
-  asm volatile("barrier.sync %0, %1;\n" ::"r"(1 + team), "r"(32 * warps) : "memory");
-}
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -104,41 +99,53 @@ __device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-// The eight codes of a word (four in each half) as bf16 pairs: 0x4180 | c << 3 is 16 + c in bf16.  One three-input
-// logic instruction a pair, its two constants in registers.  EXACT: less 24, which leaves c - 8.
+// The eight codes of a word (four in each half) as bf16 pairs of c - 8: 0x4180 | c << 3 is 16 + c in bf16, and taking 24
+// away is exact.  One three-input logic instruction a pair, its two constants in registers.
 struct Unpack {
   uint32_t mask, magic;
-  __device__ __forceinline__ Unpack() { asm volatile("mov.b32 %0, 0x00780078;\nmov.b32 %1, 0x41804180;\n" : "=r"(mask), "=r"(magic)); }
-  template <bool EXACT>
-  __device__ __forceinline__ void run(uint32_t w, uint32_t (&a)[4]) const {
-    const __nv_bfloat162 off = __halves2bfloat162(__float2bfloat16_rn(24.f), __float2bfloat16_rn(24.f));
+  __nv_bfloat162 off;
+  __device__ __forceinline__ Unpack() {
+    asm volatile("mov.b32 %0, 0x00780078;\nmov.b32 %1, 0x41804180;\n" : "=r"(mask), "=r"(magic));
+    off = __halves2bfloat162(__float2bfloat16_rn(24.f), __float2bfloat16_rn(24.f));
+  }
+  __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&a)[4]) const {
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
-      asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(a[f]) : "r"(__funnelshift_r(w, w, 4 * f)), "r"(mask), "r"(magic));  // (w & mask) | magic
-      if constexpr (EXACT) {
-        const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a[f]), off);
-        a[f] = *reinterpret_cast<const uint32_t*>(&h);
-      }
+      uint32_t v;
+      asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(v) : "r"(__funnelshift_r(w, w, 4 * f)), "r"(mask), "r"(magic));  // (w & mask) | magic
+      const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), off);
+      a[f] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
 };
 
-// A lane's inputs of 64: for each block of 32 and group of 8 rows, 8 inputs of row g of the group
+// A lane's inputs of 64: for each block of 32 and group of 8 rows, 8 inputs of row g of the group.  Past the end of K
+// (k32 blocks are left in the step) the weights are zero; the inputs there have to be too, since 0 x infinity is not.
 template <bool F32X, int RB>
 struct XUnit {
   uint4 v[2][RB][F32X ? 2 : 1];
-  // p[rb]: the lane's place in its row at the step's first input; null for a row that is not there
+  // p[rb]: the lane's place in its row at the step's first input
   __device__ __forceinline__ void load(const uint8_t* const (&p)[2], int unit, int k32) {
+    if (k32 >= 4) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
+        for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-        for (int h = 0; h < (F32X ? 2 : 1); ++h) {
-          v[b][rb][h] = make_uint4(0u, 0u, 0u, 0u);
-          if (p[rb] != nullptr && 2 * unit + b < k32)
+          for (int h = 0; h < (F32X ? 2 : 1); ++h)
             v[b][rb][h] = __ldg(reinterpret_cast<const uint4*>(p[rb] + (2 * unit + b) * (F32X ? 128 : 64) + h * 16));
-        }
+    } else {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int h = 0; h < (F32X ? 2 : 1); ++h) {
+            v[b][rb][h] = make_uint4(0u, 0u, 0u, 0u);
+            if (2 * unit + b < k32)
+              v[b][rb][h] = __ldg(reinterpret_cast<const uint4*>(p[rb] + (2 * unit + b) * (F32X ? 128 : 64) + h * 16));
+          }
+    }
   }
 };
 
@@ -151,13 +158,12 @@ __device__ __forceinline__ void scale_add(float (&acc)[4], uint32_t scales, cons
 }
 
 // acc += 64 inputs (unit U of a step) of two tiles: GP groups a step, RB groups of 8 rows.  wl: the lane's codes, sl: its
-// scales.  With one row group each block of 32 is a chain of products of its own
-// (shorter chains); with two the registers hold one chain for both blocks of a group.
+// scales.  With two row groups the blocks of a group of 64 or 128 share a chain of products (fewer additions); with one
+// the shorter chains are faster (62 against 65 us over 8 experts of 4096 x 14336 with 8 rows each).
 template <int GP, int RB, int U>
 __device__ __forceinline__ void q4_unit(float (&acc)[2][2][4], uint32_t wl, uint32_t sl, const XUnit<false, RB>& x,
                                         const Unpack& unpack) {
   constexpr int BG = GP == 4 || RB == 1 ? 1 : 2;
-  const uint32_t minus24[4] = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};
   const float zero[4] = {0.f, 0.f, 0.f, 0.f};
   uint4 w[2];
   uint32_t sc[2][GP == 4 ? 2 : 1];
@@ -167,26 +173,17 @@ __device__ __forceinline__ void q4_unit(float (&acc)[2][2][4], uint32_t wl, uint
 #pragma unroll
     for (int i = 0; i < (GP == 4 ? 2 : 1); ++i) sc[m][i] = lds32(sl + (m * GP + (GP == 4 ? 2 * U + i : (GP == 2 ? U : 0))) * 32);
   }
-  float from[2 / BG][RB][4];
-#pragma unroll
-  for (int b = 0; b < 2; ++b)
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      if (b % BG == 0) mma16816_from(from[b / BG][rb], minus24, x.v[b][rb][0].x, x.v[b][rb][0].y, zero);
-      else mma16816(from[b / BG][rb], minus24, x.v[b][rb][0].x, x.v[b][rb][0].y);
-      mma16816(from[b / BG][rb], minus24, x.v[b][rb][0].z, x.v[b][rb][0].w);
-    }
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     float d[2 / BG][RB][4];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       uint32_t a0[4], a1[4];
-      unpack.run<false>(b ? w[m].z : w[m].x, a0);
-      unpack.run<false>(b ? w[m].w : w[m].y, a1);
+      unpack(b ? w[m].z : w[m].x, a0);
+      unpack(b ? w[m].w : w[m].y, a1);
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        if (b % BG == 0) mma16816_from(d[b / BG][rb], a0, x.v[b][rb][0].x, x.v[b][rb][0].y, from[b / BG][rb]);
+        if (b % BG == 0) mma16816_from(d[b / BG][rb], a0, x.v[b][rb][0].x, x.v[b][rb][0].y, zero);
         else mma16816(d[b / BG][rb], a0, x.v[b][rb][0].x, x.v[b][rb][0].y);
         mma16816(d[b / BG][rb], a1, x.v[b][rb][0].z, x.v[b][rb][0].w);
       }
@@ -215,8 +212,8 @@ __device__ __forceinline__ void q4_unit(float (&acc)[2][2][4], uint32_t wl, uint
     uint32_t a[2][2][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      unpack.run<true>(lds32(wl + m * 1024 + U * 512 + b * 8), a[m][0]);
-      unpack.run<true>(lds32(wl + m * 1024 + U * 512 + b * 8 + 4), a[m][1]);
+      unpack(lds32(wl + m * 1024 + U * 512 + b * 8), a[m][0]);
+      unpack(lds32(wl + m * 1024 + U * 512 + b * 8 + 4), a[m][1]);
     }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
@@ -267,62 +264,10 @@ __device__ __forceinline__ Q4Piece find_piece(int i, const int* offs, const int*
 }
 
 constexpr int kStageBytes = block_bytes(32);
-constexpr int kSwapOff = kWarps * kStages * kStageBytes;  // 2 KB a warp: sums of a team
-constexpr int kOffsOff = kSwapOff + kWarps * 2048;
+constexpr int kPartOff = kWarps * kStages * kStageBytes;  // 2 KB a warp: its sums of a piece that another began
+constexpr int kOffsOff = kPartOff + kWarps * 2048;
 constexpr int kSmemBytes = 128 + kOffsOff + 2 * 260 * 4;
 static_assert(kSmemBytes <= 232448 && kStageBytes % 128 == 0, "shared-memory plan");
-
-// The value of one weight in the packed layout
-__device__ __forceinline__ float q4_value(const uint8_t* expert, const Q4Shape& sh, int group, int k, int n) {
-  const int r = k % kStepK, m = (n >> 4) & 1;
-  const uint8_t* blk = expert + sh.at(n >> 5, k / kStepK);
-  const int lane = (n & 7) * 4 + ((r & 31) >> 3);
-  const int word = ((r & 63) >> 5) * 2 + ((r & 7) >> 2), field = ((r & 3) >> 1) * 2 + ((n >> 3) & 1);
-  const uint32_t turned = *reinterpret_cast<const uint32_t*>(blk + m * 1024 + (r >> 6) * 512 + lane * 16 + word * 4);
-  const uint32_t w = turned >> 3 | turned << 29;
-  const int code = (int)((w >> (16 * (r & 1) + 4 * field)) & 15u);
-  const uint32_t sc = *reinterpret_cast<const uint32_t*>(blk + 2048 + (m * (kStepK / group) + r / group) * 32 + (n & 7) * 4);
-  return (float)(code - 8) * __uint_as_float((n & 8) ? sc & 0xffff0000u : sc << 16);  // 4 by 8 bits: exact
-}
-
-// The sums of a tile's eight rows term by term, for rows that hold an infinity or NaN and for sums that overflow on
-// the way: lane's elements as everywhere, columns g and g + 8 of rows 2t and 2t + 1.
-__device__ __noinline__ float4 sums_term_by_term(const Q4Args& a, const uint8_t* expert, int group, int n0, int row0, int rows, int lane) {
-  const Q4Shape sh(a.K, a.N, group);
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = (lane & 3) * 2 + (j & 1), n = n0 + (lane >> 2) + 8 * (j >> 1);
-    if (r >= rows || n >= a.N) continue;
-    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(a.x) + ((size_t)row0 + r) * a.ldx;
-    for (int k = 0; k < a.K; ++k) v[j] = fmaf(__bfloat162float(x[k]), q4_value(expert, sh, group, k, n), v[j]);
-  }
-  return make_float4(v[0], v[1], v[2], v[3]);
-}
-
-// Bias, activation and the store of one lane's four sums: columns n and n + 8 of `rows` of the rows row and row + 1.
-template <bool F32X>
-__device__ __forceinline__ void store_unit(const Q4Args& a, int e, int n, int row, int rows, const float (&s)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int col = n + 8 * (j >> 1);
-    if ((j & 1) >= rows || col >= a.N) continue;
-    float v = s[j];
-    if (a.bias != nullptr)
-      v += F32X ? static_cast<const float*>(a.bias)[(size_t)e * a.N + col]
-                : __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[(size_t)e * a.N + col]);
-    const size_t at = ((size_t)row + (j & 1)) * a.ldy + col;
-    if (a.bf16_out) {
-      if (a.act == MOE_ACT_GELU) v = activate<MOE_ACT_GELU, true>(v);
-      else if (a.act == MOE_ACT_SILU) v = activate<MOE_ACT_SILU, true>(v);
-      static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
-    } else {
-      if (a.act == MOE_ACT_GELU) v = activate<MOE_ACT_GELU, false>(v);
-      else if (a.act == MOE_ACT_SILU) v = activate<MOE_ACT_SILU, false>(v);
-      static_cast<float*>(a.y)[at] = v;
-    }
-  }
-}
 
 // A warp starts the copies of a block: each lane the codes that it reads itself, the first lanes the scales.
 template <int GP>
@@ -332,44 +277,106 @@ __device__ __forceinline__ void fill(uint32_t stage, const uint8_t* block, int l
   if (lane < 4 * GP) copy16(stage + 2048 + lane * 16, block + 2048 + lane * 16);
 }
 
-// acc += steps [k, k1) of a piece, whose block at step k is `block`.
-template <int GP, bool F32X, int RB>
-__device__ __forceinline__ void q4_run(const Q4Args& a, const Q4Piece& p, int k, int k1, const uint8_t* block, uint32_t ring, int lane,
-                                       const Unpack& unpack, float (&acc)[2][2][4]) {
-  constexpr int kBlk = block_bytes(kStepK / GP), ES = F32X ? 4 : 2;
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    if (k + s < k1) fill<GP>(ring + s * kStageBytes, block + (size_t)s * kBlk, lane);
+// A warp's stream of blocks: its steps [s, end) of the CTA's pieces, from the first on
+template <int GP>
+struct Q4Stream {
+  static constexpr int kBlk = block_bytes(kStepK / GP);
+  const uint8_t* block;  // of step s
+  int s, end, left;      // left: steps until the blocks go on elsewhere (another expert, or its next rows)
+  uint32_t ring, stage, fresh;
+  __device__ __forceinline__ void seek(const Q4Args& a, const Q4Piece& p, int k) {
+    block = a.w + (((size_t)p.e * a.pairs + p.pair) * a.steps + k) * kBlk;
+    left = (a.pairs - p.pair) * a.steps - k;
+  }
+  __device__ __forceinline__ void issue(const Q4Args& a, int p0, const int* offs, const int* prefix, uint32_t to, int lane) {
+    if (s < end) {
+      if (left == 0) {
+        const int i = idiv(s, a.steps);  // s is a piece's first step
+        seek(a, find_piece(p0 + i, offs, prefix, a.E, a.pairs), 0);
+      }
+      fill<GP>(to, block, lane);
+      block += kBlk;
+      --left;
+      ++s;
+    }
     copies_commit();
   }
-  block += (size_t)(kStages - 1) * kBlk;
+};
+
+// acc += steps [k, k1) of a piece, the next ones of the stream.
+template <int GP, bool F32X, int RB>
+__device__ __forceinline__ void q4_run(const Q4Args& a, const Q4Piece& p, int k, int k1, int p0, const int* offs, const int* prefix,
+                                       Q4Stream<GP>& stream, int lane, const Unpack& unpack, float (&acc)[2][2][4]) {
+  constexpr int ES = F32X ? 4 : 2;
   const uint8_t* xp[2] = {nullptr, nullptr};
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
-    const int r = rb * 8 + (lane >> 2);
-    if (r < p.rows) xp[rb] = a.x + ((size_t)p.row0 + r) * a.ldx * ES + ((size_t)k * kStepK + (lane & 3) * 8) * ES;
+    const int r = min(rb * 8 + (lane >> 2), p.rows - 1);  // a row that is not there: another's inputs, its sums are not used
+    xp[rb] = a.x + ((size_t)p.row0 + r) * a.ldx * ES + ((size_t)k * kStepK + (lane & 3) * 8) * ES;
   }
   XUnit<F32X, RB> x0, x1;
-  x0.load(xp, 0, k < k1 ? (a.K - k * kStepK) >> 5 : 0);
-  uint32_t stage = ring, fresh = ring + (kStages - 1) * kStageBytes;
-  const uint32_t last = fresh;
+  int k32 = (a.K - k * kStepK) >> 5;
+  x0.load(xp, 0, k32);
   for (; k < k1; ++k) {
-    if (k + kStages - 1 < k1) fill<GP>(fresh, block, lane);  // the stage that the step before has read
-    copies_commit();
-    block += kBlk;
+    stream.issue(a, p0, offs, prefix, stream.fresh, lane);  // into the stage that the step before has read
     copies_wait<kStages - 1>();
     __syncwarp();  // the scales have come by way of other lanes
-    const uint32_t wl = stage + lane * 16, sl = stage + 2048 + (lane >> 2) * 4;
-    x1.load(xp, 1, (a.K - k * kStepK) >> 5);
+    const uint32_t wl = stream.stage + lane * 16, sl = stream.stage + 2048 + (lane >> 2) * 4;
+    x1.load(xp, 1, k32);
     q4_unit<GP, RB, 0>(acc, wl, sl, x0, unpack);
+    if (k + 1 < k1) {
+      k32 -= 4;
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
-      if (xp[rb] != nullptr) xp[rb] += kStepK * ES;
-    x0.load(xp, 0, k + 1 < k1 ? (a.K - (k + 1) * kStepK) >> 5 : 0);
+      for (int rb = 0; rb < RB; ++rb) xp[rb] += kStepK * ES;
+      x0.load(xp, 0, k32);
+    }
     q4_unit<GP, RB, 1>(acc, wl, sl, x1, unpack);
-    fresh = stage;
-    stage = stage == last ? ring : stage + kStageBytes;
+    stream.fresh = stream.stage;
+    stream.stage = stream.stage == stream.ring + (kStages - 1) * kStageBytes ? stream.ring : stream.stage + kStageBytes;
     __syncwarp();  // every lane has read the stage
+  }
+}
+
+struct Q4Sums {
+  float v[2][2][4];  // tile, group of 8 rows
+};
+// The results of a piece: bias, activation, one rounding.  A lane holds columns g and g + 8 of each tile and rows 2t and
+// 2t + 1 of each group.
+template <int ACT, bool F32X, typename O>
+__device__ __forceinline__ void store_piece(const Q4Args& a, const Q4Piece& p, const Q4Sums& sums, int lane) {
+  const int t = lane & 3;
+  float b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = p.pair * 32 + (lane >> 2) + 8 * i;
+    b[i] = 0.f;
+    if (a.bias != nullptr && n < a.N)
+      b[i] = F32X ? static_cast<const float*>(a.bias)[(size_t)p.e * a.N + n]
+                  : __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[(size_t)p.e * a.N + n]);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = (r >> 1) * 8 + 2 * t + (r & 1);
+    if (row >= p.rows) continue;
+    O* y = static_cast<O*>(a.y) + ((size_t)p.row0 + row) * a.ldy;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = p.pair * 32 + (lane >> 2) + 8 * i;
+      const float v = activate<ACT, sizeof(O) == 2>(sums.v[i >> 1][r >> 1][(i & 1) * 2 + (r & 1)] + b[i]);
+      if (n < a.N) y[n] = (O)v;
+    }
+  }
+}
+template <bool F32X>
+__device__ __noinline__ void finish_piece(const Q4Args& a, const Q4Piece p, const Q4Sums sums, int lane) {
+  if (!F32X && a.bf16_out) {
+    if (a.act == MOE_ACT_GELU) store_piece<MOE_ACT_GELU, F32X, __nv_bfloat16>(a, p, sums, lane);
+    else if (a.act == MOE_ACT_SILU) store_piece<MOE_ACT_SILU, F32X, __nv_bfloat16>(a, p, sums, lane);
+    else store_piece<MOE_ACT_NONE, F32X, __nv_bfloat16>(a, p, sums, lane);
+  } else {
+    if (a.act == MOE_ACT_GELU) store_piece<MOE_ACT_GELU, F32X, float>(a, p, sums, lane);
+    else if (a.act == MOE_ACT_SILU) store_piece<MOE_ACT_SILU, F32X, float>(a, p, sums, lane);
+    else store_piece<MOE_ACT_NONE, F32X, float>(a, p, sums, lane);
   }
 }
 
@@ -386,77 +393,71 @@ __global__ void __launch_bounds__(32 * kWarps, 1) q4_matmul_kernel(const __grid_
   if (warp == 0) load_segments(a.offsets, a.E, a.rows_cap, kRows, 1, offs, prefix, a.status, blockIdx.x == 0);
   __syncthreads();
 
-  // this CTA's pieces [p0, p0 + n), and the number of warps that share one: the rounds that n pieces take with 16 / S
-  // teams, each of ceil(steps / S) steps and, with S > 1, about two more for joining the sums
+  // this CTA's pieces [p0, p0 + n), and this warp's steps [s0, s1) of them
   const int total = prefix[a.E] * a.pairs;
   const int base = idiv(total, gridDim.x), extra = total - base * gridDim.x;
   const int p0 = blockIdx.x * base + min((int)blockIdx.x, extra), n = base + ((int)blockIdx.x < extra);
-  int ls = 0, best = 0x7fffffff;
+  const int all = n * a.steps;
+  auto first_step = [&](int w) { return (all >> 4) * w + ((all & 15) * w >> 4); };
+  const int s0 = first_step(warp), s1 = first_step(warp + 1);
+  static_assert(kWarps == 16, "first_step");
+
+  Q4Stream<GP> stream;
+  stream.s = s0;
+  stream.end = s1;
+  stream.ring = stream.stage = sbase + warp * (kStages * kStageBytes);
+  stream.fresh = stream.ring + (kStages - 1) * kStageBytes;
+  Q4Piece p{};
+  int i = idiv(s0, a.steps), k = s0 - i * a.steps;
+  if (s0 < s1) {
+    p = find_piece(p0 + i, offs, prefix, a.E, a.pairs);
+    stream.seek(a, p, k);
+  }
+#pragma unroll 1
+  for (int s = 0; s < kStages - 1; ++s) stream.issue(a, p0, offs, prefix, stream.ring + s * kStageBytes, lane);
+  float4* parts = reinterpret_cast<float4*>(smem + kPartOff);
+  const Unpack unpack;
+  Q4Sums sums;
+  int open = 0;  // > 0: the sums are the beginning of piece p, which ends at this step of the CTA's
+  for (int s = s0; s < s1;) {
+    const int k1 = min(a.steps, k + s1 - s);
 #pragma unroll
-  for (int l = 0; l <= 4; ++l) {
-    const int cost = ((n + (16 >> l) - 1) >> (4 - l)) * (((a.steps + (1 << l) - 1) >> l) + (l ? 2 : 0));
-    if (cost < best) {
-      best = cost;
-      ls = l;
+    for (int q = 0; q < 16; ++q) sums.v[q >> 3][q >> 2 & 1][q & 3] = 0.f;
+    if (p.rows <= 8) q4_run<GP, F32X, 1>(a, p, k, k1, p0, offs, prefix, stream, lane, unpack, sums.v);
+    else q4_run<GP, F32X, 2>(a, p, k, k1, p0, offs, prefix, stream, lane, unpack, sums.v);
+    s += k1 - k;
+    if (k > 0) {  // the end (or middle) of a piece that began with another warp
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < 2 || p.rows > 8)
+          parts[(warp * 4 + q) * 32 + lane] = make_float4(sums.v[q & 1][q >> 1][0], sums.v[q & 1][q >> 1][1], sums.v[q & 1][q >> 1][2],
+                                                          sums.v[q & 1][q >> 1][3]);
+    } else if (k1 < a.steps) {
+      open = (i + 1) * a.steps;
+    } else {
+      finish_piece<F32X>(a, p, sums, lane);
+    }
+    if (s < s1) {
+      ++i;
+      k = 0;
+      p = find_piece(p0 + i, offs, prefix, a.E, a.pairs);
     }
   }
-  const int team = warp >> ls, slice = warp & ((1 << ls) - 1), teams = kWarps >> ls;
-  const int k0 = (slice * a.steps) >> ls, k1 = ((slice + 1) * a.steps) >> ls;
-
-  const uint32_t ring = sbase + warp * (kStages * kStageBytes);
-  float4* swap = reinterpret_cast<float4*>(smem + kSwapOff);
-  const Unpack unpack;
-  for (int i = team; i < n; i += teams) {
-    const Q4Piece p = find_piece(p0 + i, offs, prefix, a.E, a.pairs);
-    const uint8_t* first = a.w + (((size_t)p.e * a.pairs + p.pair) * a.steps + k0) * kBlk;
-    float acc[2][2][4] = {};  // tile, group of 8 rows
-    if (p.rows <= 8) q4_run<GP, F32X, 1>(a, p, k0, k1, first, ring, lane, unpack, acc);
-    else q4_run<GP, F32X, 2>(a, p, k0, k1, first, ring, lane, unpack, acc);
-    if (ls > 0) {
-      if (i >= teams) team_sync(team, 1 << ls);  // the swap space has been read
-      if (slice > 0) {
+  __syncthreads();
+  if (open > 0) {
+    for (int w = warp + 1; w < kWarps && first_step(w) < open; ++w) {
+      if (first_step(w) == first_step(w + 1)) continue;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (q < 2 || p.rows > 8)
-            swap[(warp * 4 + q) * 32 + lane] = make_float4(acc[q & 1][q >> 1][0], acc[q & 1][q >> 1][1], acc[q & 1][q >> 1][2], acc[q & 1][q >> 1][3]);
-      }
-      team_sync(team, 1 << ls);
-      if (slice > 0) continue;
-      for (int o = 1; o < 1 << ls; ++o) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (q >= 2 && p.rows <= 8) continue;
-          const float4 v = swap[((warp + o) * 4 + q) * 32 + lane];
-          acc[q & 1][q >> 1][0] += v.x;
-          acc[q & 1][q >> 1][1] += v.y;
-          acc[q & 1][q >> 1][2] += v.z;
-          acc[q & 1][q >> 1][3] += v.w;
-        }
+      for (int q = 0; q < 4; ++q) {
+        if (q >= 2 && p.rows <= 8) continue;
+        const float4 v = parts[(w * 4 + q) * 32 + lane];
+        sums.v[q & 1][q >> 1][0] += v.x;
+        sums.v[q & 1][q >> 1][1] += v.y;
+        sums.v[q & 1][q >> 1][2] += v.z;
+        sums.v[q & 1][q >> 1][3] += v.w;
       }
     }
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
-      const int m = q & 1, rb = q >> 1;
-      if (rb * 8 >= p.rows) continue;
-      float sum[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] = rb ? (m ? acc[1][1][j] : acc[0][1][j]) : (m ? acc[1][0][j] : acc[0][0][j]);
-      const int row0 = p.row0 + rb * 8, rows = p.rows - rb * 8, n0 = p.pair * 32 + m * 16;
-      if constexpr (!F32X) {
-        bool finite = true;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) finite = finite && (2 * t + (j & 1) >= rows || fabsf(sum[j]) < INFINITY);
-        if (__any_sync(0xffffffffu, !finite)) {
-          const float4 again = sums_term_by_term(a, a.w + (size_t)p.e * a.pairs * a.steps * kBlk, kStepK / GP, n0, row0, rows, lane);
-          const float v[4] = {again.x, again.y, again.z, again.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)  // a row's result does not depend on its neighbours: the others keep their sums
-            if (!(fabsf(sum[j]) < INFINITY)) sum[j] = v[j];
-        }
-      }
-      store_unit<F32X>(a, p.e, n0 + g, row0 + 2 * t, rows - 2 * t, sum);
-    }
+    finish_piece<F32X>(a, p, sums, lane);
   }
 }
 
@@ -512,6 +513,19 @@ __global__ void __launch_bounds__(256) q4_pack_kernel(int E, int K, int N, int g
     }
     *reinterpret_cast<uint32_t*>(dst + 2048 + (tile & 1) * gp * 32 + lane * 4) = v;
   }
+}
+
+// The value of one weight in the packed layout
+__device__ __forceinline__ float q4_value(const uint8_t* expert, const Q4Shape& sh, int group, int k, int n) {
+  const int r = k % kStepK, m = (n >> 4) & 1;
+  const uint8_t* blk = expert + sh.at(n >> 5, k / kStepK);
+  const int lane = (n & 7) * 4 + ((r & 31) >> 3);
+  const int word = ((r & 63) >> 5) * 2 + ((r & 7) >> 2), field = ((r & 3) >> 1) * 2 + ((n >> 3) & 1);
+  const uint32_t turned = *reinterpret_cast<const uint32_t*>(blk + m * 1024 + (r >> 6) * 512 + lane * 16 + word * 4);
+  const uint32_t w = turned >> 3 | turned << 29;
+  const int code = (int)((w >> (16 * (r & 1) + 4 * field)) & 15u);
+  const uint32_t sc = *reinterpret_cast<const uint32_t*>(blk + 2048 + (m * (kStepK / group) + r / group) * 32 + (n & 7) * 4);
+  return (float)(code - 8) * __uint_as_float((n & 8) ? sc & 0xffff0000u : sc << 16);  // 4 by 8 bits: exact
 }
 
 template <typename T>
@@ -594,7 +608,7 @@ cudaError_t launch_q4(const Q4Args& a, int grid, cudaStream_t st) {
 
 }  // namespace
 
-moe_status_t check_q4_matmul(const moe_q4_t* m, const void* ws, size_t ws_bytes) {
+moe_status_t check_q4_matmul(const moe_q4_t* m) {
   if (m == nullptr) return MOE_ERR_INVALID_ARG;
   const moe_status_t st = check_q4(m->E, m->K, m->N, m->group);
   if (st == MOE_ERR_INVALID_ARG || m->rows_cap < 0) return MOE_ERR_INVALID_ARG;
@@ -608,8 +622,6 @@ moe_status_t check_q4_matmul(const moe_q4_t* m, const void* ws, size_t ws_bytes)
   if (m->dtype == MOE_DTYPE_F32 && m->out_dtype != MOE_DTYPE_F32) return MOE_ERR_UNSUPPORTED;
   if (ldx % (m->dtype == MOE_DTYPE_BF16 ? 8 : 4) != 0 || m->rows_cap >= (1LL << 31) - 1024) return MOE_ERR_UNSUPPORTED;
   if (ldx >= (1LL << 31) || ldy >= (1LL << 31) || most_pieces(*m) >= 1LL << 31) return MOE_ERR_UNSUPPORTED;
-  if (ws == nullptr || misaligned(ws, 256)) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < kQ4WsBytes) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
 
@@ -719,8 +731,10 @@ moe_status_t moe_q4_matmul(const moe_q4_t* m, const int32_t* offsets, const void
                            void* y, void* ws, size_t ws_bytes, cudaStream_t stream) {
   NvtxRange nvtx_range("moe_q4_matmul");
   launch_count() = 0;
-  const moe_status_t st = check_q4_matmul(m, ws, ws_bytes);
+  const moe_status_t st = check_q4_matmul(m);
   if (st != MOE_OK) return st;
+  if (ws == nullptr || misaligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < kQ4WsBytes) return MOE_ERR_WORKSPACE;
   if (m->rows_cap == 0) return MOE_OK;
   const uintptr_t es = m->dtype == MOE_DTYPE_BF16 ? 2 : 4, os = m->out_dtype == MOE_DTYPE_BF16 ? 2 : 4;
   if (offsets == nullptr || x == nullptr || packed == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;

@@ -17,63 +17,91 @@ import torch
 import sparse_mixture_experts_23_b200 as _moe
 
 _CODES = {torch.float32: 0, torch.bfloat16: 1}  # moe_dtype_t
+try:  # the stream as the number that the C calls take: torch.cuda.current_stream() makes an object of it first
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:  # pragma: no cover
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
-
-
+# The checks run on every call, ahead of a launch that takes a few microseconds: messages are put together only
+# when one fails.
 def _dtype(t, name: str) -> int:
     code = _CODES.get(t.dtype)
-    _need(code is not None, f"{name} must be float32 or bfloat16, not {t.dtype}")
+    if code is None:
+        raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
     return code
 
 
 def _rows(t, name: str, device) -> int:
     """A matrix whose rows are contiguous; returns the elements between them."""
-    _need(t.device == device, f"{name} is on {t.device}, expected {device}")
-    _need(t.dim() == 2, f"{name} must have two dimensions")
-    if t.shape[0] <= 1:
-        _need(t.shape[1] <= 1 or t.stride(1) == 1, f"the rows of {name} must be contiguous")
-        return t.shape[1]
-    _need((t.shape[1] <= 1 or t.stride(1) == 1) and t.stride(0) >= t.shape[1],
-          f"the rows of {name} must be contiguous and must not overlap")
-    return t.stride(0)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    rows, cols = shape
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"the rows of {name} must be contiguous" + (" and must not overlap" if rows > 1 else ""))
+    if rows <= 1:
+        return cols
+    if pitch < cols:
+        raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
+    return pitch
 
 
 def _dense(t, name: str, device, dtype, shape):
     if t is None:
         return None
-    _need(t.device == device, f"{name} is on {t.device}, expected {device}")
-    _need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _need(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
 def _offsets(offsets, device):
-    _need(offsets.device == device and offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.is_contiguous()
-          and offsets.shape[0] >= 2, "offsets must be a contiguous int32 vector of E + 1 entries on x's device")
-    return offsets.data_ptr(), offsets.shape[0] - 1
+    shape = offsets.shape
+    if (offsets.dtype != torch.int32 or len(shape) != 1 or shape[0] < 2 or offsets.device != device
+            or not offsets.is_contiguous()):
+        raise ValueError("offsets must be a contiguous int32 vector of E + 1 entries on x's device")
+    return offsets.data_ptr(), shape[0] - 1
 
 
 def _status(status, device):
     if status is None:
         return None
-    _need(status.device == device and status.dtype == torch.int32 and status.numel() >= 1,
-          "status must be an int32 tensor on x's device")
+    if status.device != device or status.dtype != torch.int32 or status.numel() < 1:
+        raise ValueError("status must be an int32 tensor on x's device")
     return status.data_ptr()
+
+
+def _out(out, rows: int, N: int, like, out_dtype):
+    """The result: the caller's, checked, or a new one."""
+    if out is None:
+        return torch.empty((rows, N), dtype=out_dtype or like.dtype, device=like.device)
+    if out.shape != (rows, N):
+        raise ValueError(f"out must have shape {(rows, N)}, not {tuple(out.shape)}")
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out has another type than out_dtype")
+    return out
 
 
 def _call(where: str, device, fn, *args) -> None:
     """fn(*args, stream) with the tensors' device current."""
-    _need(device.type == "cuda", f"{where} needs CUDA tensors, not {device}")
-    if torch.cuda.current_device() == device.index:
-        code = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if device.type != "cuda":
+        raise ValueError(f"{where} needs CUDA tensors, not {device}")
+    index = device.index
+    if torch.cuda.current_device() == index:
+        code = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            code = fn(*args, torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(index):
+            code = fn(*args, _raw_stream(index))
     if code != 0:
         raise _moe.MoEError(code, where)
 
@@ -92,15 +120,13 @@ def grouped_matmul(x, W, offsets, bias=None, transpose_w: bool = False, out=None
     ldx = _rows(x, "x", device)
     optr, E = _offsets(offsets, device)
     rows, K = x.shape
-    _need(W.dim() == 3, "W must have three dimensions")
-    N = W.shape[1] if transpose_w else W.shape[2]
+    shape = W.shape
+    if len(shape) != 3:
+        raise ValueError("W must have three dimensions")
+    N = shape[1] if transpose_w else shape[2]
     wptr = _dense(W, "W", device, x.dtype, (E, N, K) if transpose_w else (E, K, N))
     bptr = _dense(bias, "bias", device, x.dtype, (E, N))
-    if out is None:
-        out = torch.empty((rows, N), dtype=out_dtype or x.dtype, device=device)
-    else:
-        _need(tuple(out.shape) == (rows, N), f"out must have shape {(rows, N)}, not {tuple(out.shape)}")
-        _need(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
+    out = _out(out, rows, N, x, out_dtype)
     ldy = _rows(out, "out", device)
     m = _moe.Matmul(E, rows, K, N, code, _dtype(out, "out"), int(transpose_w), ldx, ldy)
     _call("moe_grouped_matmul", device, _moe.load_library().moe_grouped_matmul, ctypes.byref(m), optr, x.data_ptr(), wptr,
@@ -114,11 +140,13 @@ def grouped_wgrad(x, dy, offsets, bias_grad: bool = False, dW=None, db=None, sta
     be strided.  Returns dW, or (dW, db).  Both are overwritten; an expert without rows gets zeros."""
     device = x.device
     code = _dtype(x, "x")
-    _need(dy.dtype == x.dtype, f"dy must be {x.dtype}, not {dy.dtype}")
+    if dy.dtype != x.dtype:
+        raise ValueError(f"dy must be {x.dtype}, not {dy.dtype}")
     ldx, ldy = _rows(x, "x", device), _rows(dy, "dy", device)
-    _need(dy.shape[0] == x.shape[0], "x and dy must have the same number of rows")
+    (rows, K), (dy_rows, N) = x.shape, dy.shape
+    if dy_rows != rows:
+        raise ValueError("x and dy must have the same number of rows")
     optr, E = _offsets(offsets, device)
-    (rows, K), N = x.shape, dy.shape[1]
     if dW is None:
         dW = torch.empty((E, K, N), dtype=torch.float32, device=device)
     if db is None and bias_grad:
@@ -133,16 +161,21 @@ def grouped_wgrad(x, dy, offsets, bias_grad: bool = False, dW=None, db=None, sta
 def _activation(name) -> int:
     if name is None:
         return _moe.MOE_ACT_NONE
-    _need(name in _moe.ACTIVATIONS, f"unknown activation {name!r}")
-    return _moe.ACTIVATIONS[name]
+    code = _moe.ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"unknown activation {name!r}")
+    return code
 
 
 def _like(t, name: str, like, ld=None) -> int:
     """t has like's shape and type; with ld, also that row pitch."""
-    _need(t.dtype == like.dtype, f"{name} must be {like.dtype}, not {t.dtype}")
-    _need(t.shape == like.shape, f"{name} must have shape {tuple(like.shape)}, not {tuple(t.shape)}")
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype}, not {t.dtype}")
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, not {tuple(t.shape)}")
     got = _rows(t, name, like.device)
-    _need(ld is None or like.shape[0] <= 1 or got == ld, f"the rows of {name} must be {ld} elements apart, not {got}")
+    if ld is not None and got != ld and like.shape[0] > 1:
+        raise ValueError(f"the rows of {name} must be {ld} elements apart, not {got}")
     return got
 
 
@@ -152,13 +185,13 @@ def _act(u, gate, activation, p, rng, rows):
     ld = _rows(u, "u", device)
     if gate is not None:
         _like(gate, "gate", u, ld)
-    if rng is not None:
-        _need(rng.device == device and rng.dtype in (torch.int64, torch.uint64) and rng.numel() == 2 and rng.is_contiguous(),
-              "rng must hold two 64-bit integers (seed, offset) on u's device")
-    if rows is not None:
-        _need(rows.device == device and rows.dtype == torch.int32 and rows.numel() == 1,
-              "rows must be one int32 on u's device")
-    return _moe.Act(u.shape[0], None if rows is None else rows.data_ptr(), u.shape[1], code, _activation(activation), p,
+    if rng is not None and (rng.device != device or rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2
+                            or not rng.is_contiguous()):
+        raise ValueError("rng must hold two 64-bit integers (seed, offset) on u's device")
+    if rows is not None and (rows.device != device or rows.dtype != torch.int32 or rows.numel() != 1):
+        raise ValueError("rows must be one int32 on u's device")
+    shape = u.shape
+    return _moe.Act(shape[0], None if rows is None else rows.data_ptr(), shape[1], code, _activation(activation), p,
                     None if rng is None else rng.data_ptr(), ld, 0, 0)
 
 
@@ -187,8 +220,10 @@ def act_dropout_backward(dy, u, gate=None, activation="gelu", p: float = 0.0, rn
     if du is None:
         du = torch.empty(u.shape, dtype=u.dtype, device=u.device)
     m.ld_grad = _like(du, "du", u)
-    _need(gate is not None or dgate is None, "dgate without a gate")
-    if gate is not None:
+    if gate is None:
+        if dgate is not None:
+            raise ValueError("dgate without a gate")
+    else:
         if dgate is None:
             dgate = torch.empty_strided(du.shape, du.stride(), dtype=u.dtype, device=u.device)
         _like(dgate, "dgate", u, m.ld_grad)
@@ -201,11 +236,14 @@ def q4_quantize(W, group: int = 64):
     """4-bit codes and scales of ``W [E, K, N]`` (bf16 or f32, contiguous): ``(codes uint8 [E, N, K / 2], scales bf16
     [E, K / group, N])``, with ``W[e, k, n]`` near ``scales[e, k // group, n] * (code - 8)`` and the code of an even k
     in the low half of its byte.  Symmetric: the scale is max |w| / 7 of the group, codes round to the nearest."""
-    _need(W.dim() == 3, "W must have three dimensions")
+    if W.dim() != 3:
+        raise ValueError("W must have three dimensions")
     code = _dtype(W, "W")
-    _need(W.is_contiguous(), "W must be contiguous")
+    if not W.is_contiguous():
+        raise ValueError("W must be contiguous")
     E, K, N = W.shape
-    _need(group in (32, 64, 128) and K % group == 0 and K > 0, "group must be 32, 64 or 128 and divide K")
+    if group not in (32, 64, 128) or K == 0 or K % group != 0:
+        raise ValueError("group must be 32, 64 or 128 and divide K")
     q = torch.empty((E, N, K // 2), dtype=torch.uint8, device=W.device)
     s = torch.empty((E, K // group, N), dtype=torch.bfloat16, device=W.device)
     _call("moe_q4_quantize", W.device, _moe.load_library().moe_q4_quantize, E, K, N, group, code, W.data_ptr(), q.data_ptr(),
@@ -219,12 +257,15 @@ class Q4Weights:
 
     def __init__(self, codes, scales):
         device = codes.device
-        _need(codes.dim() == 3 and codes.dtype == torch.uint8, "codes must be a uint8 [E, N, K / 2] tensor")
-        _need(scales.dim() == 3, "scales must have three dimensions")
+        if codes.dim() != 3 or codes.dtype != torch.uint8:
+            raise ValueError("codes must be a uint8 [E, N, K / 2] tensor")
+        if scales.dim() != 3:
+            raise ValueError("scales must have three dimensions")
         self.E, self.N, self.K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
         groups = scales.shape[1]
-        _need(groups > 0 and self.K % groups == 0 and self.K // groups in (32, 64, 128),
-              f"scales must be [E, K / group, N] with a group of 32, 64 or 128, not {tuple(scales.shape)} for K = {self.K}")
+        if groups == 0 or self.K % groups != 0 or self.K // groups not in (32, 64, 128):
+            raise ValueError(f"scales must be [E, K / group, N] with a group of 32, 64 or 128, not {tuple(scales.shape)} for "
+                             f"K = {self.K}")
         self.group = self.K // groups
         qptr = _dense(codes, "codes", device, torch.uint8, codes.shape)
         sptr = _dense(scales, "scales", device, torch.bfloat16, (self.E, groups, self.N))
@@ -244,7 +285,7 @@ class Q4Weights:
 
 
 def q4_workspace(device="cuda"):
-    """A workspace for ``q4_matmul`` calls that follow each other on one stream; it serves every size."""
+    """A workspace for ``q4_matmul`` calls of any size."""
     return torch.zeros(_moe.moe_q4_workspace_size(), dtype=torch.uint8, device=device)
 
 
@@ -254,27 +295,27 @@ def q4_matmul(x, W: Q4Weights, offsets, bias=None, activation=None, out=None, ou
     x ``[rows, K]`` bf16 or f32 (rows may be strided), W a ``Q4Weights``, bias ``[E, N]`` of x's type or None,
     activation "gelu", "silu" or None, ``out`` ``[rows, N]`` of x's type or ``out_dtype`` (f32 or x's; rows may be
     strided); rows past ``offsets[E]`` are not written.  Made for a few rows an expert, right for any.  ws: a
-    ``q4_workspace()`` that no call on another stream uses meanwhile (made for the call when not given); a bad
-    offset is recorded in its first word (``moe_get_device_status(ws.data_ptr())``)."""
+    ``q4_workspace()`` (made for the call when not given); a bad offset is recorded in its first word
+    (``moe_get_device_status(ws.data_ptr())``)."""
     device = x.device
     code = _dtype(x, "x")
     ldx = _rows(x, "x", device)
     optr, E = _offsets(offsets, device)
-    _need(E == W.E, f"offsets has {E} experts, W {W.E}")
-    _need(x.shape[1] == W.K, f"x must have {W.K} columns, not {x.shape[1]}")
-    _need(W.packed.device == device, f"W is on {W.packed.device}, expected {device}")
+    rows, K = x.shape
+    if E != W.E:
+        raise ValueError(f"offsets has {E} experts, W {W.E}")
+    if K != W.K:
+        raise ValueError(f"x must have {W.K} columns, not {K}")
+    if W.packed.device != device:
+        raise ValueError(f"W is on {W.packed.device}, expected {device}")
     bptr = _dense(bias, "bias", device, x.dtype, (E, W.N))
-    if out is None:
-        out = torch.empty((x.shape[0], W.N), dtype=out_dtype or x.dtype, device=device)
-    else:
-        _need(tuple(out.shape) == (x.shape[0], W.N), f"out must have shape {(x.shape[0], W.N)}, not {tuple(out.shape)}")
-        _need(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
+    out = _out(out, rows, W.N, x, out_dtype)
     ldy = _rows(out, "out", device)
     if ws is None:
         ws = q4_workspace(device)
-    else:
-        _need(ws.device == device and ws.is_contiguous(), f"ws must be a contiguous tensor on {device}")
-    m = _moe.Q4(E, x.shape[0], W.K, W.N, W.group, code, _dtype(out, "out"), _activation(activation), ldx, ldy)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    m = _moe.Q4(E, rows, K, W.N, W.group, code, _dtype(out, "out"), _activation(activation), ldx, ldy)
     _call("moe_q4_matmul", device, _moe.load_library().moe_q4_matmul, ctypes.byref(m), optr, x.data_ptr(), W.packed.data_ptr(),
           bptr, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return out

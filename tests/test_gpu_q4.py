@@ -2,8 +2,8 @@
 fp64 products of the weights that the codes stand for.
 
 Bounds.  The weights are exact (a code difference of 4 bits times a bf16 scale); a sum of K terms in fp32, cut or
-rounded at each of its additions (three a term for fp32 rows, whose parts are summed apart), the joins of at most 160
-parts and the bias: (P K + 162) 2^-23 of the summed magnitudes, P = 1 or 3.  The activation's slope is at most 1.13
+rounded at each of its additions (three a term for fp32 rows, whose parts are summed apart), the joins of at most 16
+warps' parts (162 allowed here) and the bias: (P K + 162) 2^-23 of the summed magnitudes, P = 1 or 3.  The activation's slope is at most 1.13
 in size, and its own arithmetic is within 2^-13 (bf16 results) or 48 2^-24 (fp32) of the value's terms, as in the
 tests of act_dropout (|v| <= 6 there: the inputs here are scaled to it).  Then the output type's rounding."""
 import pytest
@@ -246,9 +246,9 @@ def test_layer_in_4_bits(dtype, act, bias, routing):
            "W1": None, "W2": None}
     q1, q2 = moe.q4_quantize(randn((E, H, F), dt, 3, H ** -0.5), group), moe.q4_quantize(randn((E, F, H), dt, 4, F ** -0.5), group)
     buf = moe.MoEBuffers(moe.make_shape(T, H, E, k, F, 1.25, dtype, act, routing), inp)
-    W1, W2, ws = moe.Q4Weights(*q1), moe.Q4Weights(*q2), moe.q4_workspace()
+    W1, W2 = moe.Q4Weights(*q1), moe.Q4Weights(*q2)
     buf.out.fill_(float("nan"))
-    buf.forward_q4(W1, W2, ws)
+    buf.forward_q4(W1, W2)
     assert moe.moe_last_launch_count() == 3 and buf.device_status() == moe.MOE_OK
     ref = torch.zeros((T, H), dtype=torch.float64, device="cuda")
     w1, w2, x = dense(*q1), dense(*q2), inp["x"].double()
@@ -268,6 +268,6 @@ def test_layer_in_4_bits(dtype, act, bias, routing):
     err = (buf.out.double() - ref).abs().max()
     assert err <= (2e-2 * ref.square().mean().sqrt() if dtype == "bf16" else 1e-4 * ref.abs().max())
     fused = buf.out.clone()  # without the combine, then moe_combine
-    buf.expert_ffn_q4(W1, W2, ws, combine=False)
+    buf.expert_ffn_q4(W1, W2, combine=False)
     buf.combine()
     assert torch.equal(buf.out, fused)

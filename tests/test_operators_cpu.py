@@ -224,13 +224,13 @@ def test_q4_layer_checks():
     shape = moe.make_shape(16, 128, 4, 2, 192, dtype="bf16")
     io = moe.IO(*([FAKE] * 14))
 
-    def call(shape=shape, io=io, group=64, W1=FAKE, W2=FAKE, ws=FAKE, bytes=WS, q4ws=FAKE, q4bytes=WS, combine=1):
-        return moe.moe_expert_ffn_q4(shape, io, group, W1, W2, ws, bytes, q4ws, q4bytes, combine)
+    def call(shape=shape, io=io, group=64, W1=FAKE, W2=FAKE, ws=FAKE, bytes=WS, combine=1):
+        return moe.moe_expert_ffn_q4(shape, io, group, W1, W2, ws, bytes, combine)
 
     assert call(group=128) == moe.MOE_ERR_UNSUPPORTED  # does not divide F
     assert call(group=48) == moe.MOE_ERR_INVALID_ARG
-    assert call(bytes=100) == moe.MOE_ERR_WORKSPACE and call(q4bytes=100) == moe.MOE_ERR_WORKSPACE
-    for bad in (dict(W1=None), dict(W2=None), dict(W1=FAKE + 8), dict(ws=None), dict(q4ws=None), dict(q4ws=FAKE + 64)):
+    assert call(bytes=100) == moe.MOE_ERR_WORKSPACE
+    for bad in (dict(W1=None), dict(W2=None), dict(W1=FAKE + 8), dict(ws=None), dict(ws=FAKE + 64)):
         assert call(**bad) == moe.MOE_ERR_INVALID_ARG, bad
     no_out = moe.IO(*([FAKE] * 14))
     no_out.out = None
