@@ -1356,6 +1356,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // warp first zeroes the rows past the segment inside the last of those steps, in its own shared memory
 // and (through the cluster window) in the peer's.  Commits free the stage (and hand the accumulator to
 // the epilogue) in both CTAs at once.
+// SPLIT (moe_grouped_wgrad): the tensor core cuts where it adds, a little towards zero at each of its steps, which over
+// a thousand rows comes to 1e-6 of the result (1.4e-6 with a third of 5003 rows in one expert).  There the accumulator
+// of every kChunkStages stages (768 rows) is a sum of its own, which the epilogue adds into fp32 registers, 128 columns a
+// thread.  Eight epilogue warps in two warpgroups take registers over from the producer's and MMA issuer's for it
+// (232 and 40 a thread; with 168 for all, the sums spilled and the epilogue held the MMAs up).
 struct WgPairCfg {
   static constexpr int kTileM = 256, kTileN = 256, kStageK = 128;
   static constexpr int kStages = 3;
@@ -1370,16 +1375,25 @@ struct WgPairCfg {
   static constexpr int kOffsOff = kMiscOff + 16;
   static constexpr int kStgOff = (kOffsOff + 260 * 4 + 1023) & ~1023;
   static constexpr int kSmemBytes = 1024 + kStgOff + kEpiWarps * kStgWarpBytes;
-  static_assert(kStgOff % 16 == 0 && kSmemBytes <= 232448, "shared-memory plan");
+  static constexpr int kChunkStages = 6;
+  static constexpr int kSplitWarps = 8, kBox = 4096;  // SPLIT: epilogue warps, a staging box of 32 x 32 fp32 each
+  static constexpr int kSplitThreads = 128 + 32 * kSplitWarps;  // warps 2 and 3 only give their registers away
+  static constexpr int kSplitFew = 40, kSplitMany = 232;
+  static_assert(128 * kSplitFew + 32 * kSplitWarps * kSplitMany <= kSplitThreads * 168, "registers of the launch");
+  static constexpr int kSplitSmemBytes = 1024 + kStgOff + kSplitWarps * kBox;
+  static_assert(kStgOff % 1024 == 0 && kSmemBytes <= 232448 && kSplitSmemBytes <= 232448, "shared-memory plan");
   // kind::f16, D fp32, A and B bf16 MN-major, N = 256, M = 256 over the pair
   static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
                                      ((uint32_t)(kTileN >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
 };
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool SPLIT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT ? WgPairCfg::kSplitThreads : kThreads, 1)
     wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmD, WgradArgs g) {
   using C = WgPairCfg;
+  constexpr int EW = SPLIT ? C::kSplitWarps : kEpiWarps;  // epilogue warps
+  constexpr int EW0 = SPLIT ? 4 : 2;                      // the first of them
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -1394,7 +1408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int* offs = reinterpret_cast<int*>(smem + C::kOffsOff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* stg = reinterpret_cast<float*>(smem + C::kStgOff + (warp >= 2 ? warp - 2 : 0) * kStgWarpBytes);
+  float* stg = reinterpret_cast<float*>(smem + C::kStgOff + (warp >= EW0 ? warp - EW0 : 0) * (SPLIT ? C::kBox : kStgWarpBytes));
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
@@ -1410,7 +1424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), 2 * kEpiWarps);  // every epilogue warp of both CTAs
+      mbar_init(tempty_bar(b), 2 * EW);  // every epilogue warp of both CTAs
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -1421,7 +1435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (g.rows_cap > 0) {
     if (warp == 0) load_segments(g.offsets, E, g.rows_cap, 1, 1, offs, nullptr, g.status, blockIdx.x == 0);
   } else {
-    for (int i = threadIdx.x; i <= E; i += kThreads) offs[i] = g.offsets[i];
+    for (int i = threadIdx.x; i <= E; i += (int)blockDim.x) offs[i] = g.offsets[i];
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), C::kTmemCols);
   tc_fence_before();
@@ -1436,171 +1450,245 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     m0 = (local % MT) * C::kTileM;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer (both CTAs) -----
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int armed[C::kStages];
-      for (int s = 0; s < C::kStages; ++s) armed[s] = -1;
-      bool ok = true;
-      for (int tile = cluster_id; tile < total && ok; tile += nclusters) {
-        int e, m0, n0;
-        decode(tile, e, m0, n0);
-        const int r0 = offs[e], cnt = offs[e + 1] - r0, KB = (cnt + C::kStageK - 1) / C::kStageK;
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, g.wait_limit, abort_flag, g.status, kDevTimeoutProducer)) {
-            ok = false;
-            break;
-          }
-          const uint32_t a_dst = sbase + stage * C::kStageBytes;
-          const uint32_t b_dst = a_dst + C::kABytes;
-          const int k0 = r0 + kb * C::kStageK;
-          // both CTAs' bytes complete on the leader's full barrier, which the leader arms; rows of a
-          // ragged last stage past the segment are zeroed by the leader's MMA warp once they land
-          if (leader) {
-            mbar_arrive_expect_tx(full_bar(stage), 2 * C::kStageBytes);
-            armed[stage] = (int)phase;
-          }
-          const uint32_t fb = peer_addr(full_bar(stage), 0);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            tma_load_2d_pair(a_dst + j * C::kBoxBytes, &tmA, m0 + 128 * (int)rank + 64 * j, k0, fb);
-            tma_load_2d_pair(b_dst + j * C::kBoxBytes, &tmB, n0 + 128 * (int)rank + 64 * j, k0, fb);
-          }
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
-      if (!ok || *abort_flag) {
-        for (int s = 0; s < C::kStages; ++s)
-          if (armed[s] >= 0) {
-            volatile int dummy = 0;
-            mbar_wait(full_bar(s), (uint32_t)armed[s], g.wait_limit, &dummy, g.status, kDevTimeoutDrain);
-          }
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA (leader) ---------------
-    if (leader) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int it = 0;
-      bool ok = true;
-      bool issued = false;
-      for (int tile = cluster_id; tile < total && ok; tile += nclusters, ++it) {
-        int e, m0, n0;
-        decode(tile, e, m0, n0);
-        const int r0 = offs[e], cnt = offs[e + 1] - r0, KB = (cnt + C::kStageK - 1) / C::kStageK;
-        const int buf = it & 1;
-        const uint32_t tphase = (uint32_t)((it >> 1) & 1);
-        if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(buf), tphase ^ 1u, g.wait_limit, abort_flag, g.status,
-                                               kDevTimeoutMma))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * C::kTileN);
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, g.wait_limit, abort_flag, g.status,
-                                                 kDevTimeoutMma))) {
-            ok = false;
-            break;
-          }
-          const uint32_t a_addr = sbase + stage * C::kStageBytes;
-          const int valid = min(C::kStageK, cnt - kb * C::kStageK);
-          // a ragged last stage runs only the 16-row MMA steps that hold segment rows; the rows past the
-          // segment inside the last of them are zeroed first, in this CTA's four boxes and the peer's
-          // (whole 128-byte lines, which the swizzle leaves in place)
-          const int nk = (valid + 15) / 16;
-          if (valid < 16 * nk) {
-            const int per_box = (16 * nk - valid) * 8;  // 16-byte pieces per box
-            for (int i = lane; i < 8 * per_box; i += 32) {
-              const int box = (i / per_box) & 3, rem = i % per_box;
-              const uint32_t addr = a_addr + box * C::kBoxBytes + (valid + rem / 8) * 128 + (rem % 8) * 16;
-              if (i < 4 * per_box) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(addr), "r"(0u) : "memory");
-              else asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(peer_addr(addr, 1)), "r"(0u) : "memory");
+  if (warp < EW0) {
+    if constexpr (SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kSplitFew));
+    if (warp == 0) {
+      // ------------------------------------------------------------ TMA producer (both CTAs) -----
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        int armed[C::kStages];
+        for (int s = 0; s < C::kStages; ++s) armed[s] = -1;
+        bool ok = true;
+        for (int tile = cluster_id; tile < total && ok; tile += nclusters) {
+          int e, m0, n0;
+          decode(tile, e, m0, n0);
+          const int r0 = offs[e], cnt = offs[e + 1] - r0, KB = (cnt + C::kStageK - 1) / C::kStageK;
+          for (int kb = 0; kb < KB; ++kb) {
+            if (!mbar_wait(empty_bar(stage), phase ^ 1u, g.wait_limit, abort_flag, g.status, kDevTimeoutProducer)) {
+              ok = false;
+              break;
             }
-            asm volatile("fence.proxy.async.shared::cluster;\n" ::: "memory");
+            const uint32_t a_dst = sbase + stage * C::kStageBytes;
+            const uint32_t b_dst = a_dst + C::kABytes;
+            const int k0 = r0 + kb * C::kStageK;
+            // both CTAs' bytes complete on the leader's full barrier, which the leader arms; rows of a
+            // ragged last stage past the segment are zeroed by the leader's MMA warp once they land
+            if (leader) {
+              mbar_arrive_expect_tx(full_bar(stage), 2 * C::kStageBytes);
+              armed[stage] = (int)phase;
+            }
+            const uint32_t fb = peer_addr(full_bar(stage), 0);
+  #pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              tma_load_2d_pair(a_dst + j * C::kBoxBytes, &tmA, m0 + 128 * (int)rank + 64 * j, k0, fb);
+              tma_load_2d_pair(b_dst + j * C::kBoxBytes, &tmB, n0 + 128 * (int)rank + 64 * j, k0, fb);
+            }
+            if (++stage == C::kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          __syncwarp();
+        }
+        if (!ok || *abort_flag) {
+          for (int s = 0; s < C::kStages; ++s)
+            if (armed[s] >= 0) {
+              volatile int dummy = 0;
+              mbar_wait(full_bar(s), (uint32_t)armed[s], g.wait_limit, &dummy, g.status, kDevTimeoutDrain);
+            }
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA (leader) ---------------
+      if (leader) {
+        int stage = 0;
+        uint32_t phase = 0;
+        int it = 0;
+        bool ok = true;
+        bool issued = false;
+        for (int tile = cluster_id; tile < total && ok; tile += nclusters, ++it) {
+          int e, m0, n0;
+          decode(tile, e, m0, n0);
+          const int r0 = offs[e], cnt = offs[e + 1] - r0, KB = (cnt + C::kStageK - 1) / C::kStageK;
+          if (SPLIT && KB == 0) {
+            --it;  // no accumulator: the epilogue writes zeros
+            continue;
+          }
+          int buf = it & 1, chunk0 = 0;
+          if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(buf), (uint32_t)((it >> 1) & 1) ^ 1u, g.wait_limit, abort_flag,
+                                                 g.status, kDevTimeoutMma))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t b_addr = a_addr + C::kABytes;
-            if (nk == C::kStageK / 16) {
-#pragma unroll
-              for (int kk = 0; kk < C::kStageK / 16; ++kk)
-                mma_bf16_pair(d_tmem, desc_mnmajor(a_addr + kk * 16 * 128, C::kBoxBytes),
-                              desc_mnmajor(b_addr + kk * 16 * 128, C::kBoxBytes), C::kIdesc, (kb | kk) != 0 ? 1u : 0u);
-            } else {
-              for (int kk = 0; kk < nk; ++kk)
-                mma_bf16_pair(d_tmem, desc_mnmajor(a_addr + kk * 16 * 128, C::kBoxBytes),
-                              desc_mnmajor(b_addr + kk * 16 * 128, C::kBoxBytes), C::kIdesc, (kb | kk) != 0 ? 1u : 0u);
+          uint32_t d_tmem = tmem_base + (uint32_t)(buf * C::kTileN);
+          for (int kb = 0; kb < KB; ++kb) {
+            if (SPLIT && kb - chunk0 == C::kChunkStages) {
+              // hand this chunk's sums to the epilogue and go on in the other accumulator
+              if (elect_one()) mma_commit_both(tfull_bar(buf));
+              __syncwarp();
+              chunk0 = kb;
+              ++it;
+              buf = it & 1;
+              if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(buf), (uint32_t)((it >> 1) & 1) ^ 1u, g.wait_limit, abort_flag,
+                                                     g.status, kDevTimeoutMma))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              d_tmem = tmem_base + (uint32_t)(buf * C::kTileN);
             }
-            mma_commit_both(empty_bar(stage));  // frees this stage in both CTAs once its MMAs are done
+            if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, g.wait_limit, abort_flag, g.status,
+                                                   kDevTimeoutMma))) {
+              ok = false;
+              break;
+            }
+            const uint32_t a_addr = sbase + stage * C::kStageBytes;
+            const int valid = min(C::kStageK, cnt - kb * C::kStageK);
+            // a ragged last stage runs only the 16-row MMA steps that hold segment rows; the rows past the
+            // segment inside the last of them are zeroed first, in this CTA's four boxes and the peer's
+            // (whole 128-byte lines, which the swizzle leaves in place)
+            const int nk = (valid + 15) / 16;
+            if (valid < 16 * nk) {
+              const int per_box = (16 * nk - valid) * 8;  // 16-byte pieces per box
+              for (int i = lane; i < 8 * per_box; i += 32) {
+                const int box = (i / per_box) & 3, rem = i % per_box;
+                const uint32_t addr = a_addr + box * C::kBoxBytes + (valid + rem / 8) * 128 + (rem % 8) * 16;
+                if (i < 4 * per_box) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(addr), "r"(0u) : "memory");
+                else asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(peer_addr(addr, 1)), "r"(0u) : "memory");
+              }
+              asm volatile("fence.proxy.async.shared::cluster;\n" ::: "memory");
+            }
+            __syncwarp();
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t a_desc = desc_mnmajor(a_addr, C::kBoxBytes), b_desc = desc_mnmajor(a_addr + C::kABytes, C::kBoxBytes);
+              const uint32_t a_lo = (uint32_t)a_desc, a_hi = (uint32_t)(a_desc >> 32);
+              const uint32_t b_lo = (uint32_t)b_desc, b_hi = (uint32_t)(b_desc >> 32);
+              constexpr uint32_t kStep = 16 * 128 / 16;  // 16 contraction rows of 128 bytes, in units of 16 bytes
+              if (nk == C::kStageK / 16) {
+                mma_bf16_pair(d_tmem, a_lo, a_hi, b_lo, b_hi, C::kIdesc, kb != chunk0 ? 1u : 0u);
+#pragma unroll
+                for (int kk = 1; kk < C::kStageK / 16; ++kk)
+                  mma_bf16_pair(d_tmem, a_lo + kk * kStep, a_hi, b_lo + kk * kStep, b_hi, C::kIdesc, 1u);
+              } else {
+                for (int kk = 0; kk < nk; ++kk)
+                  mma_bf16_pair(d_tmem, a_lo + kk * kStep, a_hi, b_lo + kk * kStep, b_hi, C::kIdesc, (kb != chunk0 || kk != 0) ? 1u : 0u);
+              }
+              mma_commit_both(empty_bar(stage));  // frees this stage in both CTAs once its MMAs are done
+            }
+            issued = true;
+            __syncwarp();
+            if (++stage == C::kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          issued = true;
+          if (!ok) break;
+          if (elect_one()) mma_commit_both(tfull_bar(buf));  // with no rows this arrives at once
           __syncwarp();
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (!ok) break;
-        if (lane == 0) mma_commit_both(tfull_bar(buf));  // with no rows this arrives at once
-        __syncwarp();
-      }
-      if ((!ok || *abort_flag) && issued && lane == 0) {
-        mma_commit_pair(drain_bar);
-        volatile int dummy = 0;
-        mbar_wait(drain_bar, 0, g.wait_limit, &dummy, g.status, kDevTimeoutDrain);
+        if ((!ok || *abort_flag) && issued && elect_one()) {
+          mma_commit_pair(drain_bar);
+          volatile int dummy = 0;
+          mbar_wait(drain_bar, 0, g.wait_limit, &dummy, g.status, kDevTimeoutDrain);
+        }
       }
     }
   } else {
-    // ------------------------------------------------------------ epilogue (warps 2..5, both) --
+    if constexpr (SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kSplitMany));
+    // ------------------------------------------------------------ epilogue (warps 2..5, or 4..11, both) --
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;
+    const int half = (warp - EW0) >> 2;
     const uint32_t tempty_leader0 = peer_addr(tempty_bar(0), 0);
     const uint32_t tempty_leader1 = peer_addr(tempty_bar(1), 0);
     int it = 0;
+    uint8_t* box = reinterpret_cast<uint8_t*>(stg);  // 32 x 32 fp32, 128-byte rows, 128-byte swizzle
+    constexpr int kChunks = C::kTileN / 32 / (EW / 4);
+    // 32 columns of this warp's 32 rows of D into the box, and from there to memory (rows and columns past the edge are
+    // not written)
+    auto store32 = [&](const uint32_t* r, int col, int row0, int e) {
+      if (lane == 0) bulk_wait_read0();  // the previous box has left the staging buffer
+      __syncwarp();
+      uint8_t* row = box + lane * 128;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<uint4*>(row + ((q ^ (lane & 7)) * 16)) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&tmD, smem_u32(box), col, row0, e);
+        bulk_commit();
+      }
+    };
     for (int tile = cluster_id; tile < total; tile += nclusters, ++it) {
       int e, m0, n0;
       decode(tile, e, m0, n0);
-      const bool empty = offs[e + 1] == offs[e];
-      const int buf = it & 1;
-      const uint32_t tphase = (uint32_t)((it >> 1) & 1);
-      const bool got = mbar_wait(tfull_bar(buf), tphase, g.wait_limit, abort_flag, g.status, kDevTimeoutEpilogue);
-      if (!__all_sync(0xffffffffu, got)) break;
-      tc_fence_after();
+      const int cnt = offs[e + 1] - offs[e];
       const int row0 = m0 + 128 * (int)rank + quarter * 32;  // this warp's 32 rows of D
-      constexpr int kChunks = C::kTileN / 32 / (kEpiWarps / 4);
-      uint8_t* box = reinterpret_cast<uint8_t*>(stg);  // 32 x 32 fp32, 128-byte rows, 128-byte swizzle
-#pragma unroll 1
-      for (int c = half * kChunks; c < (half + 1) * kChunks; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * C::kTileN + c * 32), r);
-        const int col = n0 + c * 32;
-        if (row0 >= g.M || col >= g.N) continue;  // wholly past the edge (partial parts are clipped)
-        if (lane == 0) bulk_wait_read0();  // the previous box has left the staging buffer
-        __syncwarp();
-        uint8_t* row = box + lane * 128;
+      if constexpr (SPLIT) {
+        float sum[kChunks][32];  // 32 columns each
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint4 v = empty ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
-          *reinterpret_cast<uint4*>(row + ((q ^ (lane & 7)) * 16)) = v;
+        for (int q = 0; q < kChunks; ++q)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[q][j] = 0.f;
+        const int parts = (cnt + C::kChunkStages * C::kStageK - 1) / (C::kChunkStages * C::kStageK);
+        bool got = true;
+        for (int p = 0; p < parts && got; ++p) {
+          const int buf = (it + p) & 1;
+          got = __all_sync(0xffffffffu, mbar_wait(tfull_bar(buf), (uint32_t)(((it + p) >> 1) & 1), g.wait_limit, abort_flag,
+                                                  g.status, kDevTimeoutEpilogue));
+          if (!got) break;
+          tc_fence_after();
+          const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * C::kTileN + half * 128);
+#pragma unroll
+          for (int h = 0; h < kChunks; h += 2) {
+            if (row0 >= g.M || n0 + (half * kChunks + h) * 32 >= g.N) continue;  // wholly past the edge
+            uint32_t r[2][32];
+            tmem_ld32_start(taddr + h * 32, r[0]);
+            tmem_ld32_start(taddr + h * 32 + 32, r[1]);
+            tmem_wait_ld(r[0], r[1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum[h + c][j] += __uint_as_float(r[c][j]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(buf ? tempty_leader1 : tempty_leader0);
         }
-        fence_async_smem();
+        if (!got) break;
+        it += parts - 1;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const int col = n0 + (half * kChunks + c) * 32;
+          uint32_t r[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[c][j]);
+          if (row0 < g.M && col < g.N) store32(r, col, row0, e);
+        }
+      } else {
+        const int buf = it & 1;
+        const bool got = mbar_wait(tfull_bar(buf), (uint32_t)((it >> 1) & 1), g.wait_limit, abort_flag, g.status,
+                                   kDevTimeoutEpilogue);
+        if (!__all_sync(0xffffffffu, got)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = half * kChunks; c < (half + 1) * kChunks; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * C::kTileN + c * 32), r);
+          const int col = n0 + c * 32;
+          if (row0 >= g.M || col >= g.N) continue;  // wholly past the edge (partial parts are clipped)
+          if (cnt == 0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = 0u;
+          }
+          store32(r, col, row0, e);
+        }
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&tmD, smem_u32(box), col, row0, e);  // rows >= M and columns >= N are not written
-          bulk_commit();
-        }
+        if (lane == 0) mbar_arrive_cluster(buf ? tempty_leader1 : tempty_leader0);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(buf ? tempty_leader1 : tempty_leader0);
     }
     if (lane == 0) bulk_wait0();  // this warp's boxes are written before exit
   }
@@ -1838,9 +1926,15 @@ cudaError_t launch_wgrad(const void* A, const void* B, int rows_cap, int M, int 
   if (pair) {
     CUtensorMap md;
     if (!make_map_dw(&md, out, E, M, N)) return cudaErrorInvalidValue;
-    cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(wgrad_pair_kernel), WgPairCfg::kSmemBytes);
+    if (caller_offsets) {
+      cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(wgrad_pair_kernel<true>), WgPairCfg::kSplitSmemBytes);
+      if (err != cudaSuccess) return err;
+      wgrad_pair_kernel<true><<<grid & ~1, WgPairCfg::kSplitThreads, WgPairCfg::kSplitSmemBytes, st>>>(ma, mb, md, g);
+      return cudaGetLastError();
+    }
+    cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(wgrad_pair_kernel<false>), WgPairCfg::kSmemBytes);
     if (err != cudaSuccess) return err;
-    wgrad_pair_kernel<<<grid & ~1, kThreads, WgPairCfg::kSmemBytes, st>>>(ma, mb, md, g);
+    wgrad_pair_kernel<false><<<grid & ~1, kThreads, WgPairCfg::kSmemBytes, st>>>(ma, mb, md, g);
     return cudaGetLastError();
   }
   cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(wgrad_kernel), WgCfg::kSmemBytes);

@@ -202,34 +202,33 @@ __global__ void __launch_bounds__(FT) matmul_f32_kernel(F32Args a) {
 }
 
 // ---------------------------------------------------------------- bias gradient ----------------
-// db[e,n] = sum of dy[r,n] over the expert's rows.  Bound: reading dy.  A cluster of 8 blocks shares one
-// (expert, 32 x V columns) strip, its 64 warps taking every 64th row; each block adds its 8 warps' sums in
-// shared memory and block 0 the 8 blocks' through distributed shared memory, both in a fixed order, so
-// there are no atomics and the bits do not change from run to run.
-constexpr int kDbCluster = 8, kDbWarps = 8;
+// db[e,n] = sum of dy[r,n] over the expert's rows.  Bound: reading dy, or the latency of a long segment's rows.  A block
+// of 32 warps takes one (expert, 32 x V columns) strip, each warp every 32nd row with 8 of them in flight; the warps'
+// sums join in shared memory in a fixed order, so there are no atomics and the bits do not change from run to run.  (A
+// cluster of 8 blocks of 8 warps that joined through distributed shared memory took 22 us for 64 experts of 1 to 1900
+// rows of 520 columns, most of it in the cluster's barriers.)
+constexpr int kDbWarps = 32;
 
 template <typename T>
-__global__ void __cluster_dims__(1, 1, kDbCluster) __launch_bounds__(32 * kDbWarps)
+__global__ void __launch_bounds__(32 * kDbWarps)
     rows_sum_kernel(const int32_t* __restrict__ offsets, int E, long long rows_cap, const T* __restrict__ dy,
                     long long ldy, int N, float* __restrict__ db) {
   constexpr int V = 16 / sizeof(T);
   __shared__ int offs[kMaxExperts + 1];
   __shared__ float part[kDbWarps][32 * V];
-  __shared__ float sum[32 * V];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.y;
   if (warp == 0) load_segments(offsets, E, rows_cap, 1, 1, offs, nullptr, nullptr, false);
   __syncthreads();
   const int r1 = offs[e + 1], n = (blockIdx.x * 32 + lane) * V;
   float acc[V] = {};
   if (n < N) {
-    constexpr int U = 4;  // rows in flight
-    const int step = kDbCluster * kDbWarps;
-    for (long long r = (long long)offs[e] + blockIdx.z * kDbWarps + warp; r < r1; r += (long long)step * U) {
+    constexpr int U = 8;  // rows in flight
+    for (long long r = (long long)offs[e] + warp; r < r1; r += kDbWarps * U) {
       uint4 v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        v[u] = r + (long long)u * step < r1 ? __ldg(reinterpret_cast<const uint4*>(dy + (r + (long long)u * step) * ldy + n))
-                                            : make_uint4(0u, 0u, 0u, 0u);
+        v[u] = r + u * kDbWarps < r1 ? __ldg(reinterpret_cast<const uint4*>(dy + (r + u * kDbWarps) * ldy + n))
+                                     : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if constexpr (sizeof(T) == 2) {
@@ -249,33 +248,15 @@ __global__ void __cluster_dims__(1, 1, kDbCluster) __launch_bounds__(32 * kDbWar
     }
   }
 #pragma unroll
-  for (int j = 0; j < V; ++j) part[warp][lane * V + j] = acc[j];
+  for (int j = 0; j < V; ++j) part[warp][j * 32 + lane] = acc[j];
   __syncthreads();
   for (int c = threadIdx.x; c < 32 * V; c += 32 * kDbWarps) {
+    const int col = (blockIdx.x * 32 + (c & 31)) * V + (c >> 5);
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kDbWarps; ++w) s += part[w][c];
-    sum[c] = s;
+    if (col < N) db[(size_t)e * N + col] = s;
   }
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-  if (blockIdx.z == 0) {
-    for (int c = threadIdx.x; c < 32 * V; c += 32 * kDbWarps) {
-      const int col = blockIdx.x * 32 * V + c;
-      float s = 0.f;
-#pragma unroll
-      for (int b = 0; b < kDbCluster; ++b) {
-        float v;
-        asm volatile("{\n.reg .u32 ra;\nmapa.shared::cluster.u32 ra, %1, %2;\nld.shared::cluster.f32 %0, [ra];\n}\n"
-                     : "=f"(v)
-                     : "r"((uint32_t)__cvta_generic_to_shared(&sum[c])), "r"(b)
-                     : "memory");
-        s += v;
-      }
-      if (col < N) db[(size_t)e * N + col] = s;
-    }
-  }
-  // no block leaves while block 0 may still read its sums
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
 cudaError_t launch_matmul_f32(const GroupedArgs& g, cudaStream_t st) {
@@ -320,7 +301,7 @@ cudaError_t launch_wgrad_f32(const GroupedArgs& g, const float* dy, float* dW, c
 template <typename T>
 cudaError_t launch_rows_sum(const GroupedArgs& g, const void* dy, float* db, cudaStream_t st) {
   constexpr int cols = 32 * 16 / (int)sizeof(T);
-  const dim3 grid((unsigned)((g.N + cols - 1) / cols), (unsigned)g.E, kDbCluster);
+  const dim3 grid((unsigned)((g.N + cols - 1) / cols), (unsigned)g.E);
   rows_sum_kernel<T><<<grid, 32 * kDbWarps, 0, st>>>(g.offsets, g.E, g.rows_cap, static_cast<const T*>(dy), g.ldy, g.N, db);
   return cudaGetLastError();
 }
