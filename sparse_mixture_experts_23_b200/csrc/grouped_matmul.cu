@@ -19,8 +19,11 @@ namespace {
 // of shared memory per k (6 wavefronts a warp, 24 of the 64 cycles its 32 packed FMAs take on four
 // sub-partitions) and issues them as fma.rn.f32x2, two products an instruction, which leaves issue slots
 // for the loads.  64-row tiles rather than 128: ragged segments of a few dozen rows waste less of them.
-constexpr int FM = 64, FN = 128, FK = 16, FT = 128;
-constexpr int FA = FM + 4, FB = FN + 4;  // padded rows: 16-byte reads stay aligned
+// Where that gives too few tiles, 64 x 64 ones, and up to 8 groups of threads that share a tile's steps and add their
+// sums at the end: a warp or two a sub-partition leave the latency of every step open (1003 rows of 516 x 780 for 16
+// experts: 100 us with one group of 128 threads a tile, see launch_f32 for the rest).
+constexpr int FM = 64, FK = 16;
+constexpr int FA = FM + 4;  // padded rows: 16-byte reads stay aligned
 
 enum { MODE_NN = 0, MODE_NT = 1, MODE_TN = 2 };
 
@@ -43,6 +46,9 @@ __device__ __forceinline__ float4 zero4() { return make_float4(0.f, 0.f, 0.f, 0.
 __device__ __forceinline__ void fma2(unsigned long long& d, unsigned long long a, unsigned long long b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
+__device__ __forceinline__ void add2(unsigned long long& d, unsigned long long a) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(a));
+}
 __device__ __forceinline__ unsigned long long pack2(float x, float y) {
   unsigned long long r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
@@ -52,13 +58,26 @@ __device__ __forceinline__ void unpack2(unsigned long long v, float& x, float& y
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
 }
 
-template <int MODE>
-__global__ void __launch_bounds__(FT) matmul_f32_kernel(F32Args a) {
+constexpr int f32_group_floats(int fn) { return 2 * FK * (FA + fn + 4); }
+constexpr int f32_smem(int fn, int groups) {
+  const int steps = groups * f32_group_floats(fn) * 4, sums = (groups - 1) * FM * fn * 4;
+  return (steps > sums ? steps : sums);
+}
+
+template <int MODE, int FN, int KG>
+__global__ void __launch_bounds__(FN * KG) matmul_f32_kernel(F32Args a) {
+  constexpr int FT = FN, FB = FN + 4;  // threads of a group: 8 x 8 outputs each
+  constexpr int kGroup = f32_group_floats(FN);
   __shared__ int offs[kMaxExperts + 1], prefix[kMaxExperts + 1];
-  __shared__ __align__(16) float As[2][FK][FA];
-  __shared__ __align__(16) float Bs[2][FK][FB];
-  const int tid = threadIdx.x;
-  if (tid < 32)
+  extern __shared__ __align__(16) float tiles[];
+  const int tid = threadIdx.x % FT, group = threadIdx.x / FT;
+  float(*As)[FK][FA] = reinterpret_cast<float(*)[FK][FA]>(tiles + group * kGroup);
+  float(*Bs)[FK][FB] = reinterpret_cast<float(*)[FK][FB]>(tiles + group * kGroup + 2 * FK * FA);
+  auto group_sync = [&]() {
+    if constexpr (KG == 1) __syncthreads();
+    else asm volatile("barrier.sync %0, %1;\n" ::"r"(1 + group), "n"(FT) : "memory");
+  };
+  if (threadIdx.x < 32)
     load_segments(a.offsets, a.E, a.rows_cap, FM, 1, offs, MODE == MODE_TN ? nullptr : prefix, a.status,
                   blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0);
   __syncthreads();
@@ -86,12 +105,13 @@ __global__ void __launch_bounds__(FT) matmul_f32_kernel(F32Args a) {
                                      : a.B + arow0 * a.ldb + n0;
   const long long ldb = MODE == MODE_NN ? a.N : (MODE == MODE_NT ? a.K : a.ldb);
 
-  // this thread's 16-byte pieces of the next k step: 2 of A, 4 of B (K, M, N are multiples of 4, so a piece
+  // this thread's 16-byte pieces of the next k step (K, M, N are multiples of 4, so a piece
   // is wholly inside or wholly outside)
-  float4 ra[2], rb[4];
+  constexpr int PA = FM * FK / 4 / FT, PB = FN * FK / 4 / FT;
+  float4 ra[PA], rb[PB];
   auto fetch = [&](int k0) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < PA; ++j) {
       const int i = tid + j * FT;
       if constexpr (MODE == MODE_TN) {  // 16 rows of 64 columns
         const int kk = i >> 4, c = (i & 15) * 4;
@@ -104,14 +124,14 @@ __global__ void __launch_bounds__(FT) matmul_f32_kernel(F32Args a) {
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < PB; ++j) {
       const int i = tid + j * FT;
       if constexpr (MODE == MODE_NT) {
         const int r = i >> 2, kk = (i & 3) * 4;
         rb[j] = r < ncols && k0 + kk < K ? __ldg(reinterpret_cast<const float4*>(B + (long long)r * ldb + k0 + kk))
                                          : zero4();
       } else {
-        const int kk = i >> 5, c = (i & 31) * 4;
+        const int kk = i / (FN / 4), c = (i % (FN / 4)) * 4;
         rb[j] = k0 + kk < K && c < ncols ? __ldg(reinterpret_cast<const float4*>(B + (long long)(k0 + kk) * ldb + c))
                                          : zero4();
       }
@@ -119,7 +139,7 @@ __global__ void __launch_bounds__(FT) matmul_f32_kernel(F32Args a) {
   };
   auto put = [&](int s) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < PA; ++j) {
       const int i = tid + j * FT;
       if constexpr (MODE == MODE_TN) {
         *reinterpret_cast<float4*>(&As[s][i >> 4][(i & 15) * 4]) = ra[j];
@@ -132,7 +152,7 @@ __global__ void __launch_bounds__(FT) matmul_f32_kernel(F32Args a) {
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < PB; ++j) {
       const int i = tid + j * FT;
       if constexpr (MODE == MODE_NT) {
         const int r = i >> 2, kk = (i & 3) * 4;
@@ -141,28 +161,29 @@ __global__ void __launch_bounds__(FT) matmul_f32_kernel(F32Args a) {
         Bs[s][kk + 2][r] = rb[j].z;
         Bs[s][kk + 3][r] = rb[j].w;
       } else {
-        *reinterpret_cast<float4*>(&Bs[s][i >> 5][(i & 31) * 4]) = rb[j];
+        *reinterpret_cast<float4*>(&Bs[s][i / (FN / 4)][(i % (FN / 4)) * 4]) = rb[j];
       }
     }
   };
 
-  const int tx = tid & 15, ty = tid >> 4;  // columns 4 tx .. and 64 + 4 tx .., rows 8 ty ..
+  const int tx = tid % (FN / 8), ty = tid / (FN / 8);  // columns 4 tx .. and FN / 2 + 4 tx .., rows 8 ty ..
   unsigned long long acc[8][4] = {};
   int s = 0;
-  if (K > 0) {
-    fetch(0);
+  const int first = group * FK;  // a group takes every KG-th step
+  if (first < K) {
+    fetch(first);
     put(0);
   }
-  __syncthreads();
-  for (int k0 = 0; k0 < K; k0 += FK) {
-    const bool more = k0 + FK < K;
-    if (more) fetch(k0 + FK);
+  group_sync();
+  for (int k0 = first; k0 < K; k0 += KG * FK) {
+    const bool more = k0 + KG * FK < K;
+    if (more) fetch(k0 + KG * FK);
 #pragma unroll
     for (int kk = 0; kk < FK; ++kk) {
       const float4 a0 = *reinterpret_cast<const float4*>(&As[s][kk][ty * 8]);
       const float4 a1 = *reinterpret_cast<const float4*>(&As[s][kk][ty * 8 + 4]);
       const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(&Bs[s][kk][tx * 4]);
-      const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(&Bs[s][kk][64 + tx * 4]);
+      const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(&Bs[s][kk][FN / 2 + tx * 4]);
       const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -174,15 +195,34 @@ __global__ void __launch_bounds__(FT) matmul_f32_kernel(F32Args a) {
       }
     }
     if (more) put(s ^ 1);
-    __syncthreads();
+    group_sync();
     s ^= 1;
   }
+  if constexpr (KG > 1) {
+    // the groups' sums, in order
+    ulonglong2* sums = reinterpret_cast<ulonglong2*>(tiles);
+    __syncthreads();  // the tiles have been read
+    if (group > 0) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) sums[((group - 1) * 16 + q) * FT + tid] = make_ulonglong2(acc[q >> 1][2 * (q & 1)], acc[q >> 1][2 * (q & 1) + 1]);
+    }
+    __syncthreads();
+    if (group > 0) return;
+    for (int o = 0; o < KG - 1; ++o)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const ulonglong2 v = sums[(o * 16 + q) * FT + tid];
+        add2(acc[q >> 1][2 * (q & 1)], v.x);
+        add2(acc[q >> 1][2 * (q & 1) + 1], v.y);
+      }
+  }
+
 
   float* D = MODE == MODE_TN ? a.D + (size_t)e * a.M * a.N + (size_t)m0 * a.N + n0 : a.D + arow0 * a.ldd + n0;
   const long long ldd = MODE == MODE_TN ? a.N : a.ldd;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int c = h * 64 + tx * 4;
+    const int c = h * (FN / 2) + tx * 4;
     if (c >= ncols) continue;
     const float4 b = a.bias ? __ldg(reinterpret_cast<const float4*>(a.bias + (size_t)e * a.N + n0 + c)) : zero4();
 #pragma unroll
@@ -198,6 +238,114 @@ __global__ void __launch_bounds__(FT) matmul_f32_kernel(F32Args a) {
       v.w += b.w;
       *reinterpret_cast<float4*>(D + (long long)r * ldd + c) = v;
     }
+  }
+}
+
+// ---------------------------------------------------------------- fp32 products of a few rows ----
+// Up to 8 rows of an expert a block, where a 64-row tile would multiply mostly zeros.  Bound: reading W.  16 warps; x in
+// shared memory, 1024 inputs at a time.  W[E,K,N]: a lane has 4 columns (128 a block) and a warp every 16th run of 4
+// inputs, the warps' sums join in shared memory.  W[E,N,K]: a warp has 4 columns (64 a block), its lanes share the
+// inputs, 128 a step, and join by shuffles.  Both in a fixed order.
+constexpr int kFewRows = 8, kFewWarps = 16, kFewK = 1024;
+constexpr int few_cols(int mode) { return mode == MODE_NN ? 128 : 4 * kFewWarps; }
+constexpr int few_smem(int mode) {
+  const int x = kFewRows * kFewK * 4, sums = mode == MODE_NN ? kFewWarps * kFewRows * 128 * 4 : 0;
+  return x > sums ? x : sums;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(32 * kFewWarps) matmul_f32_few_kernel(F32Args a) {
+  __shared__ int offs[kMaxExperts + 1], prefix[kMaxExperts + 1];
+  extern __shared__ __align__(16) float few[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0)
+    load_segments(a.offsets, a.E, a.rows_cap, kFewRows, 1, offs, prefix, a.status, blockIdx.x == 0 && blockIdx.y == 0);
+  __syncthreads();
+  if ((int)blockIdx.x >= prefix[a.E]) return;
+  const int e = find_segment(prefix, a.E, blockIdx.x);
+  const int row0 = offs[e] + ((int)blockIdx.x - prefix[e]) * kFewRows, rows = min(kFewRows, offs[e + 1] - row0);
+  const float* x = a.A + (long long)row0 * a.lda;
+  const float* W = a.B + (size_t)e * a.K * a.N;
+  const int n0 = blockIdx.y * few_cols(MODE) + (MODE == MODE_NN ? 4 * lane : 4 * warp);  // this lane's (warp's) 4 columns
+  float acc[kFewRows][4] = {};
+  for (int k0 = 0; k0 < a.K; k0 += kFewK) {
+    const int kn = min(kFewK, a.K - k0);
+    if (k0 > 0) __syncthreads();
+    for (int i = threadIdx.x; i < kFewRows * kFewK / 4; i += 32 * kFewWarps) {
+      const int r = i / (kFewK / 4), k = 4 * (i % (kFewK / 4));
+      reinterpret_cast<float4*>(few)[i] =
+          r < rows && k < kn ? __ldg(reinterpret_cast<const float4*>(x + (long long)r * a.lda + k0 + k)) : zero4();
+    }
+    __syncthreads();
+    if (MODE == MODE_NN) {
+      if (n0 >= a.N) continue;
+#pragma unroll 2
+      for (int k = 4 * warp; k < kn; k += 4 * kFewWarps) {
+        float4 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __ldg(reinterpret_cast<const float4*>(W + (size_t)(k0 + k + j) * a.N + n0));
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r) {
+          const float4 v = *reinterpret_cast<const float4*>(few + r * kFewK + k);
+          const float xv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[r][0] = fmaf(xv[j], w[j].x, acc[r][0]);
+            acc[r][1] = fmaf(xv[j], w[j].y, acc[r][1]);
+            acc[r][2] = fmaf(xv[j], w[j].z, acc[r][2]);
+            acc[r][3] = fmaf(xv[j], w[j].w, acc[r][3]);
+          }
+        }
+      }
+    } else {
+#pragma unroll 2
+      for (int k = 4 * lane; k < kn; k += 128) {
+        float4 w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          w[c] = n0 + c < a.N ? __ldg(reinterpret_cast<const float4*>(W + (size_t)(n0 + c) * a.K + k0 + k)) : zero4();
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r) {
+          const float4 v = *reinterpret_cast<const float4*>(few + r * kFewK + k);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            acc[r][c] = fmaf(v.x, w[c].x, fmaf(v.y, w[c].y, fmaf(v.z, w[c].z, fmaf(v.w, w[c].w, acc[r][c]))));
+        }
+      }
+    }
+  }
+  if (MODE == MODE_NN) {
+    __syncthreads();  // x has been read
+#pragma unroll
+    for (int r = 0; r < kFewRows; ++r)
+      reinterpret_cast<float4*>(few)[(warp * kFewRows + r) * 32 + lane] = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kFewRows * 128; i += 32 * kFewWarps) {
+      const int r = i >> 7, n = blockIdx.y * 128 + (i & 127);
+      if (r >= rows || n >= a.N) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) v += few[w * kFewRows * 128 + i];
+      if (a.bias) v += __ldg(a.bias + (size_t)e * a.N + n);
+      a.D[(long long)(row0 + r) * a.ldd + n] = v;
+    }
+  } else {
+    // 32 sums over 32 lanes: each step halves the sums a lane keeps, until lane 4 r + c has row r, column c
+    float v[32];
+#pragma unroll
+    for (int q = 0; q < 32; ++q) v[q] = acc[q >> 2][q & 3];
+#pragma unroll
+    for (int h = 16; h > 0; h >>= 1) {
+      const bool up = lane & h;
+#pragma unroll
+      for (int q = 0; q < h; ++q) {
+        const float give = up ? v[q] : v[q + h], keep = up ? v[q + h] : v[q];
+        v[q] = keep + __shfl_xor_sync(0xffffffffu, give, h);
+      }
+    }
+    const int r = lane >> 2, n = n0 + (lane & 3);
+    if (r < rows && n < a.N)
+      a.D[(long long)(row0 + r) * a.ldd + n] = v[0] + (a.bias ? __ldg(a.bias + (size_t)e * a.N + n) : 0.f);
   }
 }
 
@@ -259,6 +407,27 @@ __global__ void __launch_bounds__(32 * kDbWarps)
   }
 }
 
+template <int MODE, int FN, int KG>
+cudaError_t launch_f32_groups(const F32Args& a, dim3 grid, cudaStream_t st) {
+  const int smem = f32_smem(FN, KG);
+  const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(matmul_f32_kernel<MODE, FN, KG>), smem);
+  if (err != cudaSuccess) return err;
+  grid.y = (unsigned)((a.N + FN - 1) / FN);
+  matmul_f32_kernel<MODE, FN, KG><<<grid, FN * KG, smem, st>>>(a);
+  return cudaGetLastError();
+}
+// rows: about how many row tiles of the grid have work.  64 x 128 tiles where they fill the GPU twice over; else 64 x 64
+// ones with as many groups as let two blocks (of 4), four (of 2) or seven (of 1) of them share an SM.
+template <int MODE>
+cudaError_t launch_f32(const F32Args& a, dim3 grid, long long rows, cudaStream_t st) {
+  const long long sms = sm_count();
+  if (rows * ((a.N + 127) / 128) >= 6 * sms) return launch_f32_groups<MODE, 128, 1>(a, grid, st);
+  const long long tiles = rows * ((a.N + 63) / 64);
+  if (tiles <= sms) return launch_f32_groups<MODE, 64, 8>(a, grid, st);
+  if (tiles <= 3 * sms) return launch_f32_groups<MODE, 64, 4>(a, grid, st);
+  return launch_f32_groups<MODE, 64, 2>(a, grid, st);
+}
+
 cudaError_t launch_matmul_f32(const GroupedArgs& g, cudaStream_t st) {
   F32Args a{};
   a.offsets = g.offsets;
@@ -274,10 +443,20 @@ cudaError_t launch_matmul_f32(const GroupedArgs& g, cudaStream_t st) {
   a.K = g.K;
   a.status = g.status;
   const long long touched = g.rows_cap < g.E ? g.rows_cap : g.E;  // upper bound on the row tiles: a ragged one each
-  const dim3 grid((unsigned)(g.rows_cap / FM + touched), (unsigned)((g.N + FN - 1) / FN));
-  if (g.transpose_w) matmul_f32_kernel<MODE_NT><<<grid, FT, 0, st>>>(a);
-  else matmul_f32_kernel<MODE_NN><<<grid, FT, 0, st>>>(a);
-  return cudaGetLastError();
+  // few rows an expert: 4 experts of 5 rows in all, 652 x 7956, 48 -> 11 us; below 8 a 64-row tile is 7/8 empty
+  if (g.rows_cap <= kFewRows * touched) {
+    const int cols = g.transpose_w ? few_cols(MODE_NT) : few_cols(MODE_NN);
+    const dim3 few_grid((unsigned)(g.rows_cap / kFewRows + touched), (unsigned)((g.N + cols - 1) / cols));
+    auto kernel = g.transpose_w ? matmul_f32_few_kernel<MODE_NT> : matmul_f32_few_kernel<MODE_NN>;
+    const int smem = g.transpose_w ? few_smem(MODE_NT) : few_smem(MODE_NN);
+    const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+    if (err != cudaSuccess) return err;
+    kernel<<<few_grid, 32 * kFewWarps, smem, st>>>(a);
+    return cudaGetLastError();
+  }
+  const dim3 grid((unsigned)(g.rows_cap / FM + touched));
+  const long long rows = g.rows_cap / FM + (touched + 1) / 2;  // half of the ragged ones
+  return g.transpose_w ? launch_f32<MODE_NT>(a, grid, rows, st) : launch_f32<MODE_NN>(a, grid, rows, st);
 }
 
 cudaError_t launch_wgrad_f32(const GroupedArgs& g, const float* dy, float* dW, cudaStream_t st) {
@@ -293,9 +472,10 @@ cudaError_t launch_wgrad_f32(const GroupedArgs& g, const float* dy, float* dW, c
   a.M = g.K;
   a.N = g.N;
   a.status = g.status;
-  const dim3 grid((unsigned)((g.K + FM - 1) / FM), (unsigned)((g.N + FN - 1) / FN), (unsigned)g.E);
-  matmul_f32_kernel<MODE_TN><<<grid, FT, 0, st>>>(a);
-  return cudaGetLastError();
+  const dim3 grid((unsigned)((g.K + FM - 1) / FM), 1, (unsigned)g.E);
+  // tiles of experts with few rows end at once: with fewer rows than a step for every expert one group is enough
+  const long long rows = g.rows_cap < (long long)FK * g.E ? 1LL << 31 : (long long)grid.x * grid.z;
+  return launch_f32<MODE_TN>(a, grid, rows, st);
 }
 
 template <typename T>

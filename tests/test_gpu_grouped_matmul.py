@@ -203,3 +203,34 @@ def test_graph_replay_and_side_stream():
     ref, mag = reference(x, W, other, None, False)
     bound = 66 * SUM_STEP * mag
     within(y, ref, bound + round_bound(ref.abs() + bound, BF))
+
+
+# fp32: a few rows an expert (more inputs than fit shared memory at once), 64-wide tiles with 8, 4 and 2 groups of threads
+# a tile, 128-wide tiles
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts,K,N", [([2, 0, 9, 1], 2052, 132), ([1], 1028, 4), ([8, 8], 1024, 260), ([0, 40, 3], 260, 68),
+                                        ([300, 0, 200], 68, 2100), ([300, 0, 200], 36, 4100), ([2000, 1900], 20, 2000)],
+                         ids=lambda v: "-".join(map(str, v)) if isinstance(v, list) else str(v))
+def test_fp32_forms(counts, K, N, trans):
+    check_forward(counts, K, N, F32, F32, trans, bias=K != 1028, pad=1, spare=9)
+
+
+@pytest.mark.parametrize("counts,K,N", [([3, 2], 132, 68), ([500, 200], 260, 300), ([90, 100, 0], 1000, 772), ([40] * 8, 516, 2052)],
+                         ids=lambda v: "-".join(map(str, v[:3])) if isinstance(v, list) else str(v))
+def test_wgrad_fp32_forms(counts, K, N):
+    check_wgrad(counts, K, N, F32, bias=False)
+
+
+@pytest.mark.parametrize("counts", [[769], [767, 768, 1], [1537, 0, 2305], [128, 3000]], ids=lambda c: "-".join(map(str, c)))
+def test_wgrad_bf16_many_rows(counts):
+    check_wgrad(counts, 264, 136, BF, bias=True, pad=1, spare=130)
+
+
+def test_wgrad_of_many_rows_keeps_its_digits():
+    """Positive terms, so that partial sums only grow: a sum of its own for every 768 rows is off by at most 48 steps of
+    the tensor core, each cut at two steps of 2^-23 of the partial sum, and joining 11 of them by 11 more."""
+    n = 8192
+    x, dy = randn((n, 64), BF, 1).abs() + 0.5, randn((n, 256), BF, 2).abs() + 0.5
+    dW = moe.grouped_wgrad(x, dy, offsets_of([n]))
+    ref = x.double().T @ dy.double()
+    within(dW[0], ref, (2 * 48 + 11) * SUM_STEP * ref)
