@@ -668,13 +668,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t a_addr = sbase + stage * C::kABytes;
           const uint32_t b_addr = sbase + C::kStages * C::kABytes + stage * C::kBBytes;
+          const uint64_t adesc = desc_a_kmajor(a_addr), bdesc = BKM ? desc_a_kmajor(b_addr) : desc_mnmajor(b_addr, BK * 128);
+          const uint32_t a_lo = (uint32_t)adesc, a_hi = (uint32_t)(adesc >> 32);
+          const uint32_t b_lo = (uint32_t)bdesc, b_hi = (uint32_t)(bdesc >> 32);
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t bdesc =
-                BKM ? desc_a_kmajor(b_addr + kk * 32) : desc_mnmajor(b_addr + kk * 16 * 128, BK * 128);
-            mma_bf16(d_tmem, desc_a_kmajor(a_addr + kk * 32), bdesc, BKM ? (C::kIdesc & ~(1u << 16)) : C::kIdesc,
-                     (kb != kb0 || kk != 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < BK / 16; ++kk)  // 16 k: 32 bytes of a K-major operand, 16 rows of an MN-major one
+            mma_bf16(d_tmem, a_lo + kk * 2, a_hi, b_lo + kk * (BKM ? 2 : 128), b_hi, BKM ? (C::kIdesc & ~(1u << 16)) : C::kIdesc,
+                     kk != 0 || kb != kb0 ? 1u : 0u);
           issued = true;
           mma_commit(empty_bar(stage));
           if (++stage == C::kStages) {
@@ -975,13 +975,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t a_addr = sbase + stage * C::kABytes;
           const uint32_t b_addr = sbase + C::kStages * C::kABytes + stage * C::kBBytes;
+          const uint64_t adesc = desc_a_kmajor(a_addr), bdesc = BKM ? desc_a_kmajor(b_addr) : desc_mnmajor(b_addr, BK * 128);
+          const uint32_t a_lo = (uint32_t)adesc, a_hi = (uint32_t)(adesc >> 32);
+          const uint32_t b_lo = (uint32_t)bdesc, b_hi = (uint32_t)(bdesc >> 32);
 #pragma unroll
           for (int kk = 0; kk < C::kStageK / 16; ++kk) {
             const int sk = kk / (BK / 16), ks = kk % (BK / 16);
-            const uint64_t bdesc = BKM ? desc_a_kmajor(b_addr + sk * C::kBSubBytes + ks * 32)
-                                       : desc_mnmajor(b_addr + sk * C::kBSubBytes + ks * 16 * 128, BK * 128);
-            mma_bf16_pair(d_tmem, desc_a_kmajor(a_addr + sk * C::kASubBytes + ks * 32), bdesc, idesc,
-                          (kb | kk) != 0 ? 1u : 0u);
+            mma_bf16_pair(d_tmem, a_lo + sk * (C::kASubBytes / 16) + ks * 2, a_hi,
+                          b_lo + sk * (C::kBSubBytes / 16) + ks * (BKM ? 2 : 128), b_hi, idesc, kk != 0 || kb != 0 ? 1u : 0u);
           }
           issued = true;
           mma_commit_both(empty_bar(stage));  // frees this stage in both CTAs once its MMAs are done
@@ -2021,12 +2022,18 @@ cudaError_t launch_rows(const GroupedArgs& a, cudaStream_t st) {
     if (!ok) return cudaErrorInvalidValue;
     return a.transpose_w ? launch_pair<EPI, true>(ma, mb, ma, g, grid, st) : launch_pair<EPI>(ma, mb, ma, g, grid, st);
   }
-  const bool small = avg < 32, spread = !small && avg < BM;
+  // the widest tile that N fills, unless there are fewer tiles than SMs: what one CTA has to bring through its K loop
+  // then sets the time (2 experts of 92 rows in all, 6688 x 192: 83 us at 256 columns, 68 at 64, and 32 with its
+  // rows in one box: a CTA issues a copy in about 64 clocks, and 8-row boxes are up to 16 a step)
+  const long long mt = a.rows_cap / BM + (a.rows_cap < a.E ? a.rows_cap : a.E);
+  int bn = a.N > 128 ? 256 : (a.N > 64 ? 128 : 64);
+  while (bn > 64 && mt * ((a.N + bn - 1) / bn) < grid) bn /= 2;
+  const bool few = mt * ((a.N + bn - 1) / bn) < grid;
+  const bool small = avg < 32, spread = !small && avg < BM && !few;
   g.a_box_rows = small ? 16 : (spread ? 8 : 0);
   g.spread_rows = spread ? 1 : 0;
   if (g.a_box_rows > 0 && !make_map_a_rows(&mas, a.x, rows, a.K, g.a_box_rows, a.ldx)) return cudaErrorInvalidValue;
   const CUtensorMap* as = g.a_box_rows > 0 ? &mas : nullptr;
-  const int bn = a.N > 128 ? 256 : (a.N > 64 ? 128 : 64);
   if (a.transpose_w) {
     if (!make_map_bk(&mb, a.W, a.E, a.N, a.K, bn)) return cudaErrorInvalidValue;
     if (bn == 256) return launch_one<256, EPI, true>(ma, mb, g, grid, st, as);
