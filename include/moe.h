@@ -476,7 +476,7 @@ typedef struct {
  * the same pitch; buffers must not overlap otherwise.  Any alignment that the type has is taken; 16-byte
  * aligned buffers with widths and pitches that 16 bytes divide run wide.  Errors: MOE_ERR_INVALID_ARG (null
  * or misaligned pointers, F < 1, rows_cap < 0, unknown type or activation, p outside [0, 1] or NaN, p > 0
- * without rng, a pitch below F), MOE_ERR_UNSUPPORTED (rows_cap or F too large), MOE_ERR_CUDA.
+ * without rng, a pitch below F, a result in place of an input with another pitch, du = dgate), MOE_ERR_UNSUPPORTED (rows_cap or F too large), MOE_ERR_CUDA.
  * No workspace, no state: any number of calls at once.  1 launch; none for rows_cap = 0. */
 MOE_API moe_status_t moe_act_dropout(const moe_act_t* m, const void* u, const void* gate, void* y, cudaStream_t stream);
 MOE_API moe_status_t moe_act_dropout_backward(const moe_act_t* m, const void* dy, const void* u, const void* gate,
@@ -502,7 +502,8 @@ MOE_API moe_status_t moe_q4_pack(int32_t E, int32_t K, int32_t N, int32_t group,
 /* W[E,K,N] = scale * (code - 8) from the packed layout, rounded once to dtype.  1 launch.
  * Errors of the three: MOE_ERR_INVALID_ARG (E outside [1, 256], K or N < 1, group not 32, 64 or 128, an unknown
  * dtype, null pointers, codes or packed not 16-byte aligned, others below their type's alignment),
- * MOE_ERR_UNSUPPORTED (K not a multiple of group, K or N above 2^24, more than 2^31 blocks), MOE_ERR_CUDA. */
+ * MOE_ERR_UNSUPPORTED (K not a multiple of group, K or N above 2^24, more than 2^31 blocks of 128 x 32 weights in
+ * an expert or a launch), MOE_ERR_CUDA. */
 MOE_API moe_status_t moe_q4_dequantize(int32_t E, int32_t K, int32_t N, int32_t group, const void* packed,
                                        moe_dtype_t dtype, void* W, cudaStream_t stream);
 
@@ -527,7 +528,8 @@ typedef struct {
  * (the weights are read once for every 16 rows of an expert).  Errors: MOE_ERR_INVALID_ARG (sizes and pointers as above; rows_cap < 0; a pitch below the row;
  * an unknown type or activation; x not 16-byte aligned, y, bias and offsets below their type's alignment; ws null
  * or misaligned), MOE_ERR_UNSUPPORTED (K not a multiple of group, ldx as above, fp32 x with a bf16 y, K or N above
- * 2^24, a pitch of 2^31 or more, rows_cap >= 2^31 - 1024, more than 2^31 pieces of 16 rows and 32 columns),
+ * 2^24, a pitch of 2^31 or more, rows_cap >= 2^31 - 1024, more than 2^31 pieces of 16 rows and 32 columns, or
+ * so many that an SM has 2^31 steps of 128 inputs),
  * MOE_ERR_WORKSPACE, MOE_ERR_CUDA.  1 launch; none for rows_cap = 0. */
 MOE_API size_t moe_q4_workspace_size(void);
 MOE_API moe_status_t moe_q4_matmul(const moe_q4_t* m, const int32_t* offsets, const void* x, const void* packed,

@@ -1105,7 +1105,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // block past the segment belong to the next expert (or were never written), so the MMA warp zeroes
 // them in shared memory after the TMA lands and before the MMAs read it.  Tiles are 128 x 256, m
 // fastest inside an n column, expert-major; an expert with no rows gets zeros.  M and N are
-// multiples of 64: partial tiles read zeros past the edge and the epilogue masks them.
+// multiples of 8: partial tiles read zeros past the edge and the epilogue masks them.
 struct WgCfg {
   static constexpr int kTileM = 128, kTileN = 256, kBK = 64;
   static constexpr int kStages = 4;

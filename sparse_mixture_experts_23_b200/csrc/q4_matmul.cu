@@ -585,6 +585,8 @@ moe_status_t check_q4(int64_t E, int64_t K, int64_t N, int group) {
   if (E < 1 || E > kMaxExperts || K < 1 || N < 1) return MOE_ERR_INVALID_ARG;
   if (group != 32 && group != 64 && group != 128) return MOE_ERR_INVALID_ARG;
   if (K % group != 0 || K > (1 << 24) || N > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  const Q4Shape q((int)K, (int)N, group);
+  if ((long long)q.pairs * q.steps >= 1LL << 31) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -622,6 +624,8 @@ moe_status_t check_q4_matmul(const moe_q4_t* m) {
   if (m->dtype == MOE_DTYPE_F32 && m->out_dtype != MOE_DTYPE_F32) return MOE_ERR_UNSUPPORTED;
   if (ldx % (m->dtype == MOE_DTYPE_BF16 ? 8 : 4) != 0 || m->rows_cap >= (1LL << 31) - 1024) return MOE_ERR_UNSUPPORTED;
   if (ldx >= (1LL << 31) || ldy >= (1LL << 31) || most_pieces(*m) >= 1LL << 31) return MOE_ERR_UNSUPPORTED;
+  // a CTA counts its steps in 32 bits (the kernel runs on 148 SMs)
+  if ((most_pieces(*m) / 128 + 1) * ((m->K + kStepK - 1) / kStepK) >= 1LL << 31) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -125,6 +125,12 @@ def test_act_pointers():
     for args in ((None, FAKE, None, FAKE, None), (FAKE, FAKE, FAKE, FAKE, None), (FAKE, FAKE, None, FAKE, FAKE)):
         assert moe.moe_act_dropout_backward(act(), *args) == moe.MOE_ERR_INVALID_ARG
     assert moe.load_library().moe_act_dropout(None, FAKE, None, FAKE, None) == moe.MOE_ERR_INVALID_ARG
+    other = FAKE + (1 << 20)
+    assert moe.moe_act_dropout(act(ld_y=72), FAKE, None, FAKE) == moe.MOE_ERR_INVALID_ARG  # in place at another pitch
+    assert moe.moe_act_dropout(act(ld_y=72), FAKE, other, other) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_act_dropout_backward(act(ld_grad=72), FAKE, other, None, FAKE) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_act_dropout_backward(act(ld_grad=72), FAKE, FAKE, other, 2 * other, other) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_act_dropout_backward(act(), FAKE, FAKE, FAKE, other, other) == moe.MOE_ERR_INVALID_ARG  # du = dgate
     assert moe.moe_act_dropout(act(rows_cap=0), None, None, None) == moe.MOE_OK
     assert ctypes.sizeof(moe.Act) == 72 and moe.Act.p.offset == 32
 
@@ -178,6 +184,8 @@ def q4(**kw):
     (dict(K=1 << 25), moe.MOE_ERR_UNSUPPORTED), (dict(N=(1 << 24) + 1), moe.MOE_ERR_UNSUPPORTED), (dict(ldx=132), moe.MOE_ERR_UNSUPPORTED),
     (dict(dtype=0, out_dtype=0, ldx=130), moe.MOE_ERR_UNSUPPORTED), (dict(dtype=0), moe.MOE_ERR_UNSUPPORTED),
     (dict(rows_cap=(1 << 31) - 1024), moe.MOE_ERR_UNSUPPORTED), (dict(ldy=1 << 31), moe.MOE_ERR_UNSUPPORTED),
+    (dict(K=1 << 24, N=1 << 24), moe.MOE_ERR_UNSUPPORTED), (dict(rows_cap=1 << 30, N=2048), moe.MOE_ERR_UNSUPPORTED),
+    (dict(rows_cap=1 << 24, K=1 << 20, N=1024), moe.MOE_ERR_UNSUPPORTED),
 ])
 def test_q4_sizes(bad, code):
     assert moe.moe_q4_matmul(q4(**bad), FAKE, FAKE, FAKE, None, FAKE, FAKE, WS) == code
