@@ -1628,11 +1628,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT ? WgPairCfg::k
       const int cnt = offs[e + 1] - offs[e];
       const int row0 = m0 + 128 * (int)rank + quarter * 32;  // this warp's 32 rows of D
       if constexpr (SPLIT) {
-        float sum[kChunks][32];  // 32 columns each
+        uint32_t sum[kChunks][32];  // fp32, 32 columns each
+        if (cnt == 0) {
 #pragma unroll
-        for (int q = 0; q < kChunks; ++q)
+          for (int q = 0; q < kChunks; ++q)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sum[q][j] = 0.f;
+            for (int j = 0; j < 32; ++j) sum[q][j] = 0u;
+        }
         const int parts = (cnt + C::kChunkStages * C::kStageK - 1) / (C::kChunkStages * C::kStageK);
         bool got = true;
         for (int p = 0; p < parts && got; ++p) {
@@ -1645,6 +1647,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT ? WgPairCfg::k
 #pragma unroll
           for (int h = 0; h < kChunks; h += 2) {
             if (row0 >= g.M || n0 + (half * kChunks + h) * 32 >= g.N) continue;  // wholly past the edge
+            if (p == 0) {
+              tmem_ld32_start(taddr + h * 32, sum[h]);
+              tmem_ld32_start(taddr + h * 32 + 32, sum[h + 1]);
+              tmem_wait_ld(sum[h], sum[h + 1]);
+              continue;
+            }
             uint32_t r[2][32];
             tmem_ld32_start(taddr + h * 32, r[0]);
             tmem_ld32_start(taddr + h * 32 + 32, r[1]);
@@ -1652,7 +1660,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT ? WgPairCfg::k
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-              for (int j = 0; j < 32; ++j) sum[h + c][j] += __uint_as_float(r[c][j]);
+              for (int j = 0; j < 32; ++j)
+                sum[h + c][j] = __float_as_uint(__uint_as_float(sum[h + c][j]) + __uint_as_float(r[c][j]));
           }
           tc_fence_before();
           __syncwarp();
@@ -1663,10 +1672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPLIT ? WgPairCfg::k
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           const int col = n0 + (half * kChunks + c) * 32;
-          uint32_t r[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[c][j]);
-          if (row0 < g.M && col < g.N) store32(r, col, row0, e);
+          if (row0 < g.M && col < g.N) store32(sum[c], col, row0, e);
         }
       } else {
         const int buf = it & 1;
