@@ -522,7 +522,10 @@ __device__ __forceinline__ void router_epilogue(const GemmArgs& g, uint32_t tadd
 }
 
 
-template <int BN, int EPI, bool BKM>
+// KSPLIT (EPI_ROWS_* only): for fewer tiles than SMs.  A cluster of k_splits CTAs takes one tile, each a part of its K
+// range; then every CTA collects its share of the tile's columns from all of them through distributed shared memory
+// (the stage ring is free by then), adds them in rank order and stores them.
+template <int BN, int EPI, bool BKM, bool KSPLIT = false>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmA16, GemmArgs g) {
@@ -583,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // work items: every tile, or every (tile, K part) with split K
   const int KS = g.k_splits > 1 ? g.k_splits : 1;
   const int total = prefix[E] * KS;
+  bool summed = false;  // KSPLIT: this CTA's accumulator is there
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer -----------------
@@ -710,6 +714,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool got = mbar_wait(tfull_bar(buf), tphase, g.wait_limit, abort_flag, g.status, kDevTimeoutEpilogue);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
+      if constexpr (KSPLIT) {
+        summed = true;
+        break;
+      }
       const bool row_ok = r_in_tile < rows;
       const int grow = row0 + r_in_tile;
       float wgt = 0.f;
@@ -766,6 +774,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if constexpr (KSPLIT) {
+    __syncwarp();
+    static_assert(kEpiWarps == 4 && epi_rows(EPI), "one epilogue warp for each lane quarter");
+    const int W = BN / KS;  // columns of a CTA's share
+    const int rank = (int)cluster_ctarank(), row = (warp & 3) * 32 + lane;
+    cluster_sync_all();  // every CTA's MMAs have read their stages
+    if (warp >= 2 && summed) {
+#pragma unroll 1
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(c * 32), r);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const int col = c * 32 + j;
+          const uint32_t to = peer_addr(sbase + (uint32_t)(((rank * BM + row) * W + col % W) * 4), (uint32_t)(col / W));
+          asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(r[j]), "r"(r[j + 1]), "r"(r[j + 2]),
+                       "r"(r[j + 3])
+                       : "memory");
+        }
+      }
+    }
+    cluster_sync_all();
+    if (warp >= 2 && summed) {
+      int e, m_local, n_idx, row0, rows;
+      decode_tile((int)blockIdx.x / KS, prefix, offs, E, NT, e, m_local, n_idx, row0, rows);
+      const float4* part = reinterpret_cast<const float4*>(smem) + row * (W / 4);
+      for (int j = 0; j < W; j += 8) {
+        const int n = n_idx * BN + rank * W + j;
+        if (row >= rows || n >= g.N) break;
+        float v[8] = {};
+        for (int o = 0; o < KS; ++o) {
+          const float4 p0 = part[o * BM * (W / 4) + j / 4], p1 = part[o * BM * (W / 4) + j / 4 + 1];
+          v[0] += p0.x, v[1] += p0.y, v[2] += p0.z, v[3] += p0.w, v[4] += p1.x, v[5] += p1.y, v[6] += p1.z, v[7] += p1.w;
+        }
+        const uint4 bb = bias8(g.bias ? g.bias + (size_t)e * g.N : nullptr, n);
+        const uint32_t bw[4] = {bb.x, bb.y, bb.z, bb.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[2 * q] += __uint_as_float(bw[q] << 16);
+          v[2 * q + 1] += __uint_as_float(bw[q] & 0xffff0000u);
+        }
+        const size_t at = (size_t)(row0 + row) * g.ldo + n;
+        if constexpr (EPI == EPI_ROWS_BF16) {
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+            w[q] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          *reinterpret_cast<uint4*>(g.h_out + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          *reinterpret_cast<float4*>(g.y + at) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(g.y + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
   __syncwarp();
@@ -2001,6 +2066,27 @@ cudaError_t launch_bwd_gemms_sm100(const BwdGemmArgs& a, cudaStream_t st, int* l
   return cudaSuccess;
 }
 
+// A launch of the KSPLIT form: tiles x splits CTAs in clusters of `splits`.
+template <int EPI, bool BKM>
+cudaError_t launch_split(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mas, const GemmArgs& g, int tiles,
+                         cudaStream_t st) {
+  auto* kernel = grouped_gemm_kernel<64, EPI, BKM, true>;
+  const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), Cfg<64>::kSmemBytes);
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = (unsigned)g.k_splits;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3((unsigned)(tiles * g.k_splits));
+  config.blockDim = dim3(kThreads);
+  config.dynamicSmemBytes = Cfg<64>::kSmemBytes;
+  config.stream = st;
+  config.attrs = &cluster;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, ma, mb, mas, g);
+}
+
 // The plain grouped product (moe_grouped_matmul).  Tiles as for the FFN's GEMMs: CTA pairs where an expert
 // fills a pair tile on average, else single-CTA tiles with the row placement for short segments.
 template <int EPI>
@@ -2023,7 +2109,10 @@ cudaError_t launch_rows(const GroupedArgs& a, cudaStream_t st) {
   const int grid = sm_count();
   CUtensorMap ma, mb, mas;
   if (!make_map_a(&ma, a.x, rows, a.K, a.ldx)) return cudaErrorInvalidValue;
-  if (avg >= PairCfg::kTileM && pair_mode_enabled()) {
+  // (pair tiles on less than a quarter of the SMs: the smaller ones below, with K split, are faster: 1 expert of 300 rows,
+  // 8192 x 512, 45 -> 14 us)
+  const long long pair_tiles = (a.rows_cap / PairCfg::kTileM + (a.rows_cap < a.E ? a.rows_cap : a.E)) * ((a.N + 255) / 256);
+  if (avg >= PairCfg::kTileM && 8 * pair_tiles >= grid && pair_mode_enabled()) {
     const bool ok = a.transpose_w ? make_map_bk(&mb, a.W, a.E, a.N, a.K, PairCfg::kHalfN) : make_map_b(&mb, a.W, a.E, a.K, a.N);
     if (!ok) return cudaErrorInvalidValue;
     return a.transpose_w ? launch_pair<EPI, true>(ma, mb, ma, g, grid, st) : launch_pair<EPI>(ma, mb, ma, g, grid, st);
@@ -2040,6 +2129,19 @@ cudaError_t launch_rows(const GroupedArgs& a, cudaStream_t st) {
   g.spread_rows = spread ? 1 : 0;
   if (g.a_box_rows > 0 && !make_map_a_rows(&mas, a.x, rows, a.K, g.a_box_rows, a.ldx)) return cudaErrorInvalidValue;
   const CUtensorMap* as = g.a_box_rows > 0 ? &mas : nullptr;
+  // K in 2 to 8 parts of 4 blocks at least where that many more CTAs fit (the same case: 32 -> 11 us)
+  const long long tiles = mt * ((a.N + 63) / 64);
+  int splits = 1;
+  while (bn == 64 && splits < 8 && 2 * splits * tiles <= grid && (a.K + BK - 1) / BK >= 8 * splits) splits *= 2;
+  if (splits > 1) {
+    g.k_splits = splits;
+    if (a.transpose_w) {
+      if (!make_map_bk(&mb, a.W, a.E, a.N, a.K, 64)) return cudaErrorInvalidValue;
+      return launch_split<EPI, true>(ma, mb, as ? mas : ma, g, (int)tiles, st);
+    }
+    if (!make_map_b(&mb, a.W, a.E, a.K, a.N)) return cudaErrorInvalidValue;
+    return launch_split<EPI, false>(ma, mb, as ? mas : ma, g, (int)tiles, st);
+  }
   if (a.transpose_w) {
     if (!make_map_bk(&mb, a.W, a.E, a.N, a.K, bn)) return cudaErrorInvalidValue;
     if (bn == 256) return launch_one<256, EPI, true>(ma, mb, g, grid, st, as);

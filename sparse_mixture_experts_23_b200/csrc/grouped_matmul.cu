@@ -352,18 +352,20 @@ __global__ void __launch_bounds__(32 * kFewWarps) matmul_f32_few_kernel(F32Args 
 // ---------------------------------------------------------------- bias gradient ----------------
 // db[e,n] = sum of dy[r,n] over the expert's rows.  Bound: reading dy, or the latency of a long segment's rows.  A block
 // of 32 warps takes one (expert, 32 x V columns) strip, each warp every 32nd row with 8 of them in flight; the warps'
-// sums join in shared memory in a fixed order, so there are no atomics and the bits do not change from run to run.  (A
-// cluster of 8 blocks of 8 warps that joined through distributed shared memory took 22 us for 64 experts of 1 to 1900
-// rows of 520 columns, most of it in the cluster's barriers.)
+// sums join in shared memory in a fixed order, so there are no atomics and the bits do not change from run to run.
+// Where there are fewer strips than SMs, a cluster of 8 blocks shares a strip's rows and joins its sums through
+// distributed shared memory, since one SM reads about 95 GB/s (8000 rows of 520 columns: 44 us in 3 blocks, 8 in
+// 24).  Otherwise its barriers cost more than they save (64 experts of 1 to 1900 rows: 22 us, 14 without).
 constexpr int kDbWarps = 32;
 
-template <typename T>
-__global__ void __launch_bounds__(32 * kDbWarps)
+template <typename T, int S>
+__global__ void __cluster_dims__(1, 1, S) __launch_bounds__(32 * kDbWarps)
     rows_sum_kernel(const int32_t* __restrict__ offsets, int E, long long rows_cap, const T* __restrict__ dy,
                     long long ldy, int N, float* __restrict__ db) {
   constexpr int V = 16 / sizeof(T);
   __shared__ int offs[kMaxExperts + 1];
   __shared__ float part[kDbWarps][32 * V];
+  __shared__ float sum[32 * V];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.y;
   if (warp == 0) load_segments(offsets, E, rows_cap, 1, 1, offs, nullptr, nullptr, false);
   __syncthreads();
@@ -371,12 +373,13 @@ __global__ void __launch_bounds__(32 * kDbWarps)
   float acc[V] = {};
   if (n < N) {
     constexpr int U = 8;  // rows in flight
-    for (long long r = (long long)offs[e] + warp; r < r1; r += kDbWarps * U) {
+    constexpr int step = kDbWarps * S;
+    for (long long r = (long long)offs[e] + blockIdx.z * kDbWarps + warp; r < r1; r += step * U) {
       uint4 v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        v[u] = r + u * kDbWarps < r1 ? __ldg(reinterpret_cast<const uint4*>(dy + (r + u * kDbWarps) * ldy + n))
-                                     : make_uint4(0u, 0u, 0u, 0u);
+        v[u] = r + u * step < r1 ? __ldg(reinterpret_cast<const uint4*>(dy + (r + u * step) * ldy + n))
+                                 : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if constexpr (sizeof(T) == 2) {
@@ -398,13 +401,30 @@ __global__ void __launch_bounds__(32 * kDbWarps)
 #pragma unroll
   for (int j = 0; j < V; ++j) part[warp][j * 32 + lane] = acc[j];
   __syncthreads();
-  for (int c = threadIdx.x; c < 32 * V; c += 32 * kDbWarps) {
-    const int col = (blockIdx.x * 32 + (c & 31)) * V + (c >> 5);
-    float s = 0.f;
+  const int c = threadIdx.x;
+  const int col = (blockIdx.x * 32 + (c & 31)) * V + (c >> 5);
+  float s = 0.f;
+  if (c < 32 * V) {
 #pragma unroll
     for (int w = 0; w < kDbWarps; ++w) s += part[w][c];
-    if (col < N) db[(size_t)e * N + col] = s;
   }
+  if constexpr (S > 1) {
+    if (c < 32 * V) sum[c] = s;
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    if (blockIdx.z == 0 && c < 32 * V) {
+      for (int b = 1; b < S; ++b) {
+        float v;
+        asm volatile("{\n.reg .u32 ra;\nmapa.shared::cluster.u32 ra, %1, %2;\nld.shared::cluster.f32 %0, [ra];\n}\n"
+                     : "=f"(v)
+                     : "r"((uint32_t)__cvta_generic_to_shared(&sum[c])), "r"(b)
+                     : "memory");
+        s += v;
+      }
+    }
+    // no block leaves while block 0 may still read its sums
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  }
+  if (blockIdx.z == 0 && c < 32 * V && col < N) db[(size_t)e * N + col] = s;
 }
 
 template <int MODE, int FN, int KG>
@@ -482,7 +502,11 @@ template <typename T>
 cudaError_t launch_rows_sum(const GroupedArgs& g, const void* dy, float* db, cudaStream_t st) {
   constexpr int cols = 32 * 16 / (int)sizeof(T);
   const dim3 grid((unsigned)((g.N + cols - 1) / cols), (unsigned)g.E);
-  rows_sum_kernel<T><<<grid, 32 * kDbWarps, 0, st>>>(g.offsets, g.E, g.rows_cap, static_cast<const T*>(dy), g.ldy, g.N, db);
+  const T* d = static_cast<const T*>(dy);
+  if ((long long)grid.x * grid.y < sm_count() && g.rows_cap >= 32LL * kDbWarps)
+    rows_sum_kernel<T, 8><<<dim3(grid.x, grid.y, 8), 32 * kDbWarps, 0, st>>>(g.offsets, g.E, g.rows_cap, d, g.ldy, g.N, db);
+  else
+    rows_sum_kernel<T, 1><<<grid, 32 * kDbWarps, 0, st>>>(g.offsets, g.E, g.rows_cap, d, g.ldy, g.N, db);
   return cudaGetLastError();
 }
 

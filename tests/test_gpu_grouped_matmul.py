@@ -234,3 +234,19 @@ def test_wgrad_of_many_rows_keeps_its_digits():
     dW = moe.grouped_wgrad(x, dy, offsets_of([n]))
     ref = x.double().T @ dy.double()
     within(dW[0], ref, (2 * 48 + 11) * SUM_STEP * ref)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_bias_gradient_of_long_segments(dtype):
+    """Few strips and many rows: the rows of a strip shared by a cluster."""
+    check_wgrad([1200, 0, 300], 8, 72, dtype, bias=True, pad=1, spare=7)
+    check_wgrad([3000], 8, 520, dtype, bias=True)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts", [[1], [5, 0, 40], [128, 3], [300], [17, 100, 129]], ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("K,N", [(512, 8), (520, 64), (1096, 72), (4104, 200), (2048, 520)])
+def test_few_tiles_of_a_long_contraction(counts, K, N, trans):
+    """K shared by the CTAs of a cluster, in 2, 4 or 8 parts."""
+    check_forward(counts, K, N, BF, BF, trans, bias=N != 64, pad=1, spare=40)
+    check_forward(counts, K, N, BF, F32, trans, bias=N != 72, spare=3, seed=4)
