@@ -327,16 +327,25 @@ __device__ __forceinline__ void epilogue_h_rows(const GemmArgs& g, const uint32_
 // values pass through the warp's staging box in the same swizzle (16-byte piece j of row i at j ^ (i % 8):
 // writes and reads are free of bank conflicts), so that 8 lanes store one row's 128 contiguous bytes.  Row i
 // is output row grow0 + off_i as in epilogue_chunk; rows past the segment and columns past N (multiples of
-// 8: whole pieces) are skipped.  The rounding to bf16 is the output type's own, once, after the bias.
+// 8: whole pieces) are skipped.  The rounding to bf16 is the output type's own, once, after the bias, whose 8 pieces of
+// these columns are at `bias` in shared memory (rows_bias) or absent.  On tiles of a short K this epilogue sets the pace.
+// The bias of a tile's up to 256 columns, 16 bytes a lane, into the kilobyte behind the warp's staging box: loaded before
+// the wait for the accumulator, in place of 8 loads behind it for every 64 columns.
+__device__ __forceinline__ const uint4* rows_bias(uint8_t* stg, const __nv_bfloat16* brow, int n0, int cols, int N, int lane) {
+  if (brow == nullptr) return nullptr;
+  uint4* to = reinterpret_cast<uint4*>(stg + 4096);
+  if (8 * lane < cols) to[lane] = n0 + 8 * lane < N ? bias8(brow, n0 + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
+  __syncwarp();
+  return to;
+}
 template <bool SPREAD>
 __device__ __forceinline__ void epilogue_rows_bf16(const GemmArgs& g, const uint32_t (&r0)[32], const uint32_t (&r1)[32],
-                                                   uint8_t* stg, int lane, int grow0, int nrows,
-                                                   const __nv_bfloat16* brow, int n0) {
+                                                   uint8_t* stg, int lane, int grow0, int nrows, const uint4* bias, int n0) {
   uint8_t* row = stg + lane * 128;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const uint32_t* src = j < 4 ? &r0[8 * j] : &r1[8 * (j - 4)];
-    const uint4 bb = n0 + 8 * j < g.N ? bias8(brow, n0 + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4 bb = bias ? bias[j] : make_uint4(0u, 0u, 0u, 0u);
     const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&bb);
     uint32_t w[4];
 #pragma unroll
@@ -354,6 +363,7 @@ __device__ __forceinline__ void epilogue_rows_bf16(const GemmArgs& g, const uint
   for (int p = 0; p < 8; ++p) {
     const int i = 4 * p + (lane >> 3);
     const int off = SPREAD ? 32 * (i >> 3) + (i & 7) : i;
+    if ((SPREAD ? 32 * (p >> 1) + 4 * (p & 1) : 4 * p) >= nrows) break;  // the group's first row: no later group has any
     const uint4 v = *reinterpret_cast<const uint4*>(stg + i * 128 + ((piece ^ (i & 7)) * 16));
     if (off < nrows && n < g.N) *reinterpret_cast<uint4*>(g.h_out + (size_t)(grow0 + off) * g.ldo + n) = v;
   }
@@ -710,6 +720,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       decode_tile(tile / KS, prefix, offs, E, NT, e, m_local, n_idx, row0, rows);
       const int buf = it & 1;
       const uint32_t tphase = (uint32_t)((it >> 1) & 1);
+      const uint4* rbias = nullptr;
+      if constexpr (EPI == EPI_ROWS_BF16 && !KSPLIT)
+        rbias = rows_bias(reinterpret_cast<uint8_t*>(stg), g.bias ? g.bias + (size_t)e * g.N : nullptr, n_idx * BN, BN, g.N, lane);
       // every lane waits; the warp leaves together if any lane gave up (tcgen05.ld is warp-wide)
       const bool got = mbar_wait(tfull_bar(buf), tphase, g.wait_limit, abort_flag, g.status, kDevTimeoutEpilogue);
       if (!__all_sync(0xffffffffu, got)) break;
@@ -743,10 +756,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (wrows <= 0 || n0 >= g.N) break;
           uint32_t r0[32], r1[32];
           const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN + c * 32);
-          tmem_ld32(taddr, r0);
-          tmem_ld32(taddr + 32, r1);
-          if (spread) epilogue_rows_bf16<true>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, row0 + wbase, wrows, brow, n0);
-          else epilogue_rows_bf16<false>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, row0 + wbase, wrows, brow, n0);
+          tmem_ld32_start(taddr, r0);
+          tmem_ld32_start(taddr + 32, r1);
+          tmem_wait_ld(r0, r1);
+          const uint4* b8 = rbias ? rbias + c * 4 : nullptr;
+          if (spread) epilogue_rows_bf16<true>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, row0 + wbase, wrows, b8, n0);
+          else epilogue_rows_bf16<false>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, row0 + wbase, wrows, b8, n0);
         }
       } else
 #pragma unroll 1
@@ -1080,6 +1095,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       decode_tile_m(tile, prefix, offs, E, NT, C::kTileM, e, m_local, n_idx, row0, rows);
       const int buf = it & 1;
       const uint32_t tphase = (uint32_t)((it >> 1) & 1);
+      const uint4* rbias = nullptr;
+      if constexpr (EPI == EPI_ROWS_BF16)
+        rbias = rows_bias(reinterpret_cast<uint8_t*>(stg), g.bias ? g.bias + (size_t)e * g.N : nullptr, n_idx * C::kTileN, C::kTileN,
+                          g.N, lane);
       const bool got = mbar_wait(tfull_bar(buf), tphase, g.wait_limit, abort_flag, g.status, kDevTimeoutEpilogue);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
@@ -1123,9 +1142,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int n0 = n_idx * C::kTileN + colbase + c * 32;
           if (wrows <= 0 || n0 >= g.N) break;
           uint32_t r0[32], r1[32];
-          tmem_ld32(taddr + c * 32, r0);
-          tmem_ld32(taddr + (c + 1) * 32, r1);
-          epilogue_rows_bf16<false>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, wrow0, wrows, brow, n0);
+          tmem_ld32_start(taddr + c * 32, r0);
+          tmem_ld32_start(taddr + (c + 1) * 32, r1);
+          tmem_wait_ld(r0, r1);
+          epilogue_rows_bf16<false>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, wrow0, wrows,
+                                    rbias ? rbias + (colbase + c * 32) / 8 : nullptr, n0);
         }
       } else if constexpr (epi_dgrad(EPI)) {
         float dw = 0.f;
@@ -2110,7 +2131,7 @@ cudaError_t launch_rows(const GroupedArgs& a, cudaStream_t st) {
   CUtensorMap ma, mb, mas;
   if (!make_map_a(&ma, a.x, rows, a.K, a.ldx)) return cudaErrorInvalidValue;
   // (pair tiles on less than a quarter of the SMs: the smaller ones below, with K split, are faster: 1 expert of 300 rows,
-  // 8192 x 512, 45 -> 14 us)
+  // 8192 x 512, 45 -> 16 us)
   const long long pair_tiles = (a.rows_cap / PairCfg::kTileM + (a.rows_cap < a.E ? a.rows_cap : a.E)) * ((a.N + 255) / 256);
   if (avg >= PairCfg::kTileM && 8 * pair_tiles >= grid && pair_mode_enabled()) {
     const bool ok = a.transpose_w ? make_map_bk(&mb, a.W, a.E, a.N, a.K, PairCfg::kHalfN) : make_map_b(&mb, a.W, a.E, a.K, a.N);
