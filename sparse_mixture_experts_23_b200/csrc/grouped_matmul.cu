@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(FN * KG) matmul_f32_kernel(F32Args a) {
 // shared memory, 1024 inputs at a time.  W[E,K,N]: a lane has 4 columns (128 a block) and a warp every 16th run of 4
 // inputs, the warps' sums join in shared memory.  W[E,N,K]: a warp has 4 columns (64 a block), its lanes share the
 // inputs, 128 a step, and join by shuffles.  Both in a fixed order.
-constexpr int kFewRows = 8, kFewWarps = 16, kFewK = 1024;
+constexpr int kFewRows = 8, kFewWarps = 16, kFewK = 1024, kFewAvg = 16;
 constexpr int few_cols(int mode) { return mode == MODE_NN ? 128 : 4 * kFewWarps; }
 constexpr int few_smem(int mode) {
   const int x = kFewRows * kFewK * 4, sums = mode == MODE_NN ? kFewWarps * kFewRows * 128 * 4 : 0;
@@ -463,8 +463,10 @@ cudaError_t launch_matmul_f32(const GroupedArgs& g, cudaStream_t st) {
   a.K = g.K;
   a.status = g.status;
   const long long touched = g.rows_cap < g.E ? g.rows_cap : g.E;  // upper bound on the row tiles: a ragged one each
-  // few rows an expert: 4 experts of 5 rows in all, 652 x 7956, 48 -> 11 us; below 8 a 64-row tile is 7/8 empty
-  if (g.rows_cap <= kFewRows * touched) {
+  // Few rows an expert: 4 experts of 5 rows in all, 652 x 7956, 48 -> 11 us; a 64-row tile would stay nearly empty.  These
+  // blocks against the tiles at 15 rows an expert: 16 experts of 2048 x 1408 100 and 200 us, 60 of them 361 and 465,
+  // 126 of 712 x 1000 229 and 261 (318 and 270 with W transposed); at 30 rows: 162 and 201, 615 and 468, 396 and 225.
+  if (g.rows_cap <= kFewAvg * touched) {
     const int cols = g.transpose_w ? few_cols(MODE_NT) : few_cols(MODE_NN);
     const dim3 few_grid((unsigned)(g.rows_cap / kFewRows + touched), (unsigned)((g.N + cols - 1) / cols));
     auto kernel = g.transpose_w ? matmul_f32_few_kernel<MODE_NT> : matmul_f32_few_kernel<MODE_NN>;
