@@ -9,6 +9,7 @@
 
 #include "moe_internal.cuh"
 #include "segments.cuh"
+#include "sm100_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -21,7 +22,9 @@ namespace {
 // for the loads.  64-row tiles rather than 128: ragged segments of a few dozen rows waste less of them.
 // Where that gives too few tiles, 64 x 64 ones, and up to 8 groups of threads that share a tile's steps and add their
 // sums at the end: a warp or two a sub-partition leave the latency of every step open (1003 rows of 516 x 780 for 16
-// experts: 100 us with one group of 128 threads a tile, see launch_f32 for the rest).
+// experts: 100 us with one group of 128 threads a tile, see launch_f32 for the rest).  Where even those leave SMs idle
+// and the contraction is long, a cluster's blocks share it and add their sums through distributed shared memory, each a
+// share of them, in the blocks' order (f32_parts).
 constexpr int FM = 64, FK = 16;
 constexpr int FA = FM + 4;  // padded rows: 16-byte reads stay aligned
 
@@ -38,6 +41,7 @@ struct F32Args {
   float* D;
   long long ldd;
   int M, N, K;  // TN: M x N per expert, contraction over its rows; else N columns, contraction K
+  int parts;    // blocks of a cluster (along z) that share a tile's contraction: 1, 2, 4 or 8
   int32_t* status;
 };
 
@@ -58,9 +62,22 @@ __device__ __forceinline__ void unpack2(unsigned long long v, float& x, float& y
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
 }
 
+// this thread's four sums of the same shared-memory words in every block of the cluster, added in the blocks' order
+__device__ __forceinline__ ulonglong2 cluster_sum(const ulonglong2* own, int parts) {
+  ulonglong2 sum = make_ulonglong2(0ull, 0ull);
+  for (int b = 0; b < parts; ++b) {
+    const uint32_t at = sm100::peer_addr((uint32_t)__cvta_generic_to_shared(own), (uint32_t)b);
+    ulonglong2 v;
+    asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];\n" : "=l"(v.x), "=l"(v.y) : "r"(at) : "memory");
+    add2(sum.x, v.x);
+    add2(sum.y, v.y);
+  }
+  return sum;
+}
+
 constexpr int f32_group_floats(int fn) { return 2 * FK * (FA + fn + 4); }
 constexpr int f32_smem(int fn, int groups) {
-  const int steps = groups * f32_group_floats(fn) * 4, sums = (groups - 1) * FM * fn * 4;
+  const int steps = groups * f32_group_floats(fn) * 4, sums = (groups - (groups < 8)) * FM * fn * 4;  // 8: its own too
   return (steps > sums ? steps : sums);
 }
 
@@ -81,10 +98,11 @@ __global__ void __launch_bounds__(FN * KG) matmul_f32_kernel(F32Args a) {
     load_segments(a.offsets, a.E, a.rows_cap, FM, 1, offs, MODE == MODE_TN ? nullptr : prefix, a.status,
                   blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0);
   __syncthreads();
+  const int parts = KG == 8 ? a.parts : 1;
   int e, m0, mrows, K;  // mrows: valid output rows of the tile
   long long arow0;      // first A row of the tile (NN, NT), first contraction row (TN)
   if constexpr (MODE == MODE_TN) {
-    e = blockIdx.z;
+    e = blockIdx.z / parts;
     m0 = blockIdx.x * FM;
     mrows = min(FM, a.M - m0);
     arow0 = offs[e];
@@ -104,6 +122,12 @@ __global__ void __launch_bounds__(FN * KG) matmul_f32_kernel(F32Args a) {
                    : MODE == MODE_NT ? a.B + (size_t)e * a.K * a.N + (size_t)n0 * a.K
                                      : a.B + arow0 * a.ldb + n0;
   const long long ldb = MODE == MODE_NN ? a.N : (MODE == MODE_NT ? a.K : a.ldb);
+  if (KG == 8 && parts > 1) {  // this block's share of the contraction
+    const int share = (K + parts * FK - 1) / (parts * FK) * FK, k0 = (int)(blockIdx.z % parts) * share;
+    A += MODE == MODE_TN ? k0 * a.lda : k0;
+    B += MODE == MODE_NT ? k0 : k0 * ldb;
+    K = min(share, K - k0);  // 0 or less: nothing left
+  }
 
   // this thread's 16-byte pieces of the next k step (K, M, N are multiples of 4, so a piece
   // is wholly inside or wholly outside)
@@ -207,19 +231,48 @@ __global__ void __launch_bounds__(FN * KG) matmul_f32_kernel(F32Args a) {
       for (int q = 0; q < 16; ++q) sums[((group - 1) * 16 + q) * FT + tid] = make_ulonglong2(acc[q >> 1][2 * (q & 1)], acc[q >> 1][2 * (q & 1) + 1]);
     }
     __syncthreads();
-    if (group > 0) return;
-    for (int o = 0; o < KG - 1; ++o)
+    if (group == 0) {
+      for (int o = 0; o < KG - 1; ++o)
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const ulonglong2 v = sums[(o * 16 + q) * FT + tid];
-        add2(acc[q >> 1][2 * (q & 1)], v.x);
-        add2(acc[q >> 1][2 * (q & 1) + 1], v.y);
-      }
+        for (int q = 0; q < 16; ++q) {
+          const ulonglong2 v = sums[(o * 16 + q) * FT + tid];
+          add2(acc[q >> 1][2 * (q & 1)], v.x);
+          add2(acc[q >> 1][2 * (q & 1) + 1], v.y);
+        }
+    }
   }
-
 
   float* D = MODE == MODE_TN ? a.D + (size_t)e * a.M * a.N + (size_t)m0 * a.N + n0 : a.D + arow0 * a.ldd + n0;
   const long long ldd = MODE == MODE_TN ? a.N : a.ldd;
+  if constexpr (KG == 8) {
+    if (parts > 1) {
+      // the blocks' sums, 16 bytes a thread: block p finishes pieces 16 p / parts .. of every thread's 16
+      ulonglong2* mine = reinterpret_cast<ulonglong2*>(tiles + (KG - 1) * FM * FN);
+      if (group == 0) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) mine[q * FT + tid] = make_ulonglong2(acc[q >> 1][2 * (q & 1)], acc[q >> 1][2 * (q & 1) + 1]);
+      }
+      sm100::cluster_sync_all();
+      const int part = blockIdx.z % parts;
+      const int q = part * (16 / parts) + group, c = (q & 1) * (FN / 2) + tx * 4, r = ty * 8 + (q >> 1);
+      if (group < 16 / parts && c < ncols && r < mrows) {
+        const ulonglong2 sum = cluster_sum(mine + q * FT + tid, parts);
+        const float4 b = a.bias ? __ldg(reinterpret_cast<const float4*>(a.bias + (size_t)e * a.N + n0 + c)) : zero4();
+        float4 v;
+        unpack2(sum.x, v.x, v.y);
+        unpack2(sum.y, v.z, v.w);
+        v.x += b.x;
+        v.y += b.y;
+        v.z += b.z;
+        v.w += b.w;
+        *reinterpret_cast<float4*>(D + (long long)r * ldd + c) = v;
+      }
+      __syncwarp();
+      sm100::cluster_sync_all();  // no block leaves while another may still read its sums
+      return;
+    }
+  }
+  if (group > 0) return;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int c = h * (FN / 2) + tx * 4;
@@ -245,7 +298,8 @@ __global__ void __launch_bounds__(FN * KG) matmul_f32_kernel(F32Args a) {
 // Up to 8 rows of an expert a block, where a 64-row tile would multiply mostly zeros.  Bound: reading W.  16 warps; x in
 // shared memory, 1024 inputs at a time.  W[E,K,N]: a lane has 4 columns (128 a block) and a warp every 16th run of 4
 // inputs, the warps' sums join in shared memory.  W[E,N,K]: a warp has 4 columns (64 a block), its lanes share the
-// inputs, 128 a step, and join by shuffles.  Both in a fixed order.
+// inputs, 128 a step, and join by shuffles.  Both in a fixed order.  A cluster's blocks share a long K where there are few
+// (f32_parts).
 constexpr int kFewRows = 8, kFewWarps = 16, kFewK = 1024, kFewAvg = 16;
 constexpr int few_cols(int mode) { return mode == MODE_NN ? 128 : 4 * kFewWarps; }
 constexpr int few_smem(int mode) {
@@ -267,10 +321,12 @@ __global__ void __launch_bounds__(32 * kFewWarps) matmul_f32_few_kernel(F32Args 
   const float* x = a.A + (long long)row0 * a.lda;
   const float* W = a.B + (size_t)e * a.K * a.N;
   const int n0 = blockIdx.y * few_cols(MODE) + (MODE == MODE_NN ? 4 * lane : 4 * warp);  // this lane's (warp's) 4 columns
+  const int parts = a.parts, part = blockIdx.z;
+  const int share = (a.K + 128 * parts - 1) / (128 * parts) * 128, kfirst = part * share, kend = min(a.K, kfirst + share);
   float acc[kFewRows][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += kFewK) {
-    const int kn = min(kFewK, a.K - k0);
-    if (k0 > 0) __syncthreads();
+  for (int k0 = kfirst; k0 < kend; k0 += kFewK) {
+    const int kn = min(kFewK, kend - k0);
+    if (k0 > kfirst) __syncthreads();
     for (int i = threadIdx.x; i < kFewRows * kFewK / 4; i += 32 * kFewWarps) {
       const int r = i / (kFewK / 4), k = 4 * (i % (kFewK / 4));
       reinterpret_cast<float4*>(few)[i] =
@@ -326,6 +382,10 @@ __global__ void __launch_bounds__(32 * kFewWarps) matmul_f32_few_kernel(F32Args 
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < kFewWarps; ++w) v += few[w * kFewRows * 128 + i];
+      if (parts > 1) {
+        few[i] = v;  // nobody else reads these words
+        continue;
+      }
       if (a.bias) v += __ldg(a.bias + (size_t)e * a.N + n);
       a.D[(long long)(row0 + r) * a.ldd + n] = v;
     }
@@ -344,8 +404,28 @@ __global__ void __launch_bounds__(32 * kFewWarps) matmul_f32_few_kernel(F32Args 
       }
     }
     const int r = lane >> 2, n = n0 + (lane & 3);
-    if (r < rows && n < a.N)
+    if (parts > 1) {
+      __syncthreads();  // x has been read
+      few[r * few_cols(MODE) + 4 * warp + (lane & 3)] = v[0];
+    } else if (r < rows && n < a.N)
       a.D[(long long)(row0 + r) * a.ldd + n] = v[0] + (a.bias ? __ldg(a.bias + (size_t)e * a.N + n) : 0.f);
+  }
+  if (parts > 1) {
+    // the blocks' sums, 4 columns a thread, each block its share of them
+    constexpr int pieces = kFewRows * few_cols(MODE) / 4;
+    __syncwarp();
+    sm100::cluster_sync_all();
+    const int i = part * (pieces / parts) + threadIdx.x, r = i / (few_cols(MODE) / 4), c = i % (few_cols(MODE) / 4) * 4;
+    const int n = blockIdx.y * few_cols(MODE) + c;
+    if ((int)threadIdx.x < pieces / parts && r < rows && n < a.N) {
+      const ulonglong2 sum = cluster_sum(reinterpret_cast<const ulonglong2*>(few) + i, parts);
+      float4 v, b = a.bias ? __ldg(reinterpret_cast<const float4*>(a.bias + (size_t)e * a.N + n)) : zero4();
+      unpack2(sum.x, v.x, v.y);
+      unpack2(sum.y, v.z, v.w);
+      *reinterpret_cast<float4*>(a.D + (long long)(row0 + r) * a.ldd + n) = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+    }
+    __syncwarp();
+    sm100::cluster_sync_all();  // no block leaves while another may still read its sums
   }
 }
 
@@ -427,29 +507,60 @@ __global__ void __cluster_dims__(1, 1, S) __launch_bounds__(32 * kDbWarps)
   if (blockIdx.z == 0 && c < 32 * V && col < N) db[(size_t)e * N + col] = s;
 }
 
+// kernel on clusters of a.parts blocks along z
+template <typename Kernel>
+cudaError_t launch_parts(Kernel* kernel, const F32Args& a, dim3 grid, int threads, int smem, cudaStream_t st) {
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = cluster.val.clusterDim.y = 1;
+  cluster.val.clusterDim.z = (unsigned)a.parts;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(grid.x, grid.y, grid.z * (unsigned)a.parts);
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = st;
+  config.attrs = &cluster;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, a);
+}
+
+// How many blocks share a contraction of k: 1, 2, 4 or 8, as long as they all find an SM at once and a share keeps
+// `least` of it.  One expert of 7000 x 640: 40 rows 186 -> 29 us in 8 parts; 8192 x 64, 10 rows 82 -> 13; 64 rows of
+// 8000 x 2000 224 -> 112 in 4; 60 rows of 1200 x 300 37 -> 14.  With more blocks than SMs, clusters of 8 fill only about
+// 128 of them and take longer than whole tiles: 200 rows of 4000 x 2000 169 and 111 us.
+int f32_parts(long long blocks, long long k, int least) {
+  int parts = 1;
+  while (parts < 8 && 2 * parts * blocks <= sm_count() && k >= 2LL * parts * least) parts *= 2;
+  return parts;
+}
+
 template <int MODE, int FN, int KG>
 cudaError_t launch_f32_groups(const F32Args& a, dim3 grid, cudaStream_t st) {
   const int smem = f32_smem(FN, KG);
   const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(matmul_f32_kernel<MODE, FN, KG>), smem);
   if (err != cudaSuccess) return err;
   grid.y = (unsigned)((a.N + FN - 1) / FN);
-  matmul_f32_kernel<MODE, FN, KG><<<grid, FN * KG, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_parts(matmul_f32_kernel<MODE, FN, KG>, a, grid, FN * KG, smem, st);
 }
 // rows: about how many row tiles of the grid have work.  64 x 128 tiles where they fill the GPU twice over; else 64 x 64
 // ones with as many groups as let two blocks (of 4), four (of 2) or seven (of 1) of them share an SM.
+// k: how long the contraction is, about.
 template <int MODE>
-cudaError_t launch_f32(const F32Args& a, dim3 grid, long long rows, cudaStream_t st) {
+cudaError_t launch_f32(F32Args a, dim3 grid, long long rows, long long k, cudaStream_t st) {
   const long long sms = sm_count();
   if (rows * ((a.N + 127) / 128) >= 6 * sms) return launch_f32_groups<MODE, 128, 1>(a, grid, st);
   const long long tiles = rows * ((a.N + 63) / 64);
-  if (tiles <= sms) return launch_f32_groups<MODE, 64, 8>(a, grid, st);
+  if (tiles <= sms) {
+    a.parts = f32_parts(tiles, k, 256);
+    return launch_f32_groups<MODE, 64, 8>(a, grid, st);
+  }
   if (tiles <= 3 * sms) return launch_f32_groups<MODE, 64, 4>(a, grid, st);
   return launch_f32_groups<MODE, 64, 2>(a, grid, st);
 }
 
 cudaError_t launch_matmul_f32(const GroupedArgs& g, cudaStream_t st) {
   F32Args a{};
+  a.parts = 1;
   a.offsets = g.offsets;
   a.E = g.E;
   a.rows_cap = g.rows_cap;
@@ -469,20 +580,21 @@ cudaError_t launch_matmul_f32(const GroupedArgs& g, cudaStream_t st) {
   if (g.rows_cap <= kFewAvg * touched) {
     const int cols = g.transpose_w ? few_cols(MODE_NT) : few_cols(MODE_NN);
     const dim3 few_grid((unsigned)(g.rows_cap / kFewRows + touched), (unsigned)((g.N + cols - 1) / cols));
+    a.parts = f32_parts((long long)few_grid.x * few_grid.y, g.K, 512);
     auto kernel = g.transpose_w ? matmul_f32_few_kernel<MODE_NT> : matmul_f32_few_kernel<MODE_NN>;
     const int smem = g.transpose_w ? few_smem(MODE_NT) : few_smem(MODE_NN);
     const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
     if (err != cudaSuccess) return err;
-    kernel<<<few_grid, 32 * kFewWarps, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_parts(kernel, a, few_grid, 32 * kFewWarps, smem, st);
   }
   const dim3 grid((unsigned)(g.rows_cap / FM + touched));
   const long long rows = g.rows_cap / FM + (touched + 1) / 2;  // half of the ragged ones
-  return g.transpose_w ? launch_f32<MODE_NT>(a, grid, rows, st) : launch_f32<MODE_NN>(a, grid, rows, st);
+  return g.transpose_w ? launch_f32<MODE_NT>(a, grid, rows, g.K, st) : launch_f32<MODE_NN>(a, grid, rows, g.K, st);
 }
 
 cudaError_t launch_wgrad_f32(const GroupedArgs& g, const float* dy, float* dW, cudaStream_t st) {
   F32Args a{};
+  a.parts = 1;
   a.offsets = g.offsets;
   a.E = g.E;
   a.rows_cap = g.rows_cap;
@@ -497,7 +609,7 @@ cudaError_t launch_wgrad_f32(const GroupedArgs& g, const float* dy, float* dW, c
   const dim3 grid((unsigned)((g.K + FM - 1) / FM), 1, (unsigned)g.E);
   // tiles of experts with few rows end at once: with fewer rows than a step for every expert one group is enough
   const long long rows = g.rows_cap < (long long)FK * g.E ? 1LL << 31 : (long long)grid.x * grid.z;
-  return launch_f32<MODE_TN>(a, grid, rows, st);
+  return launch_f32<MODE_TN>(a, grid, rows, g.rows_cap / g.E, st);
 }
 
 template <typename T>

@@ -221,6 +221,21 @@ def test_wgrad_fp32_forms(counts, K, N):
     check_wgrad(counts, K, N, F32, bias=False)
 
 
+# a tile's contraction shared by 2, 4 and 8 blocks, with shares that end early and tiles that end inside
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts,K,N", [([1], 1024, 4), ([3, 0, 6], 4100, 36), ([9], 2308, 300), ([5, 11], 1028, 1156), ([40], 516, 68),
+                                        ([0, 70], 2052, 132), ([129], 1028, 700), ([33, 90], 8004, 60)],
+                         ids=lambda v: "-".join(map(str, v)) if isinstance(v, list) else str(v))
+def test_fp32_few_tiles_of_a_long_contraction(counts, K, N, trans):
+    check_forward(counts, K, N, F32, F32, trans, bias=K != 1028, pad=1, spare=9)
+
+
+@pytest.mark.parametrize("counts,K,N", [([513], 4, 4), ([2048], 68, 132), ([0, 3000], 64, 64), ([600, 1, 900], 132, 260)],
+                         ids=lambda v: "-".join(map(str, v)) if isinstance(v, list) else str(v))
+def test_wgrad_fp32_few_tiles_of_many_rows(counts, K, N):
+    check_wgrad(counts, K, N, F32, bias=True, pad=1, spare=5)
+
+
 @pytest.mark.parametrize("counts", [[769], [767, 768, 1], [1537, 0, 2305], [128, 3000]], ids=lambda c: "-".join(map(str, c)))
 def test_wgrad_bf16_many_rows(counts):
     check_wgrad(counts, 264, 136, BF, bias=True, pad=1, spare=130)
