@@ -432,11 +432,12 @@ typedef struct {
  * or written, and recorded in status.  Rows of y in [offsets[E], rows_cap), and columns [N, ldy), are
  * left as they were.  status: an optional (NULL) device int32, 4-byte aligned and 0 before its first
  * use, where a bad offset or a bounded wait that ran out is recorded for moe_get_device_status.
- * bf16: tcgen05 tensor cores; fp32: CUDA cores.  Each y element is one sum in a fixed order.
+ * bf16: tcgen05 tensor cores; fp32: CUDA cores.  Sums run in an order that sizes, types and the GPU fix:
+ * the same call gives the same bits.
  * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers - 16 bytes, offsets and status 4 - E
- * outside [1, 256], rows_cap < 0, K or N < 1, ld below the row length, unknown types);
+ * outside [1, 256], rows_cap < 0, K or N < 1, ld below the row length, unknown types, y = x, W or bias);
  * MOE_ERR_UNSUPPORTED (bf16: K, N, ldx or ldy not a multiple of 8; fp32: of 4; rows_cap
- * >= 2^31 - 1024, N > 4194240 or more than 2^31 output tiles; fp32 x with a bf16 y: bf16 x takes either
+ * >= 2^31 - 1024, K > 2^30, N > 4194240 or more than 2^31 output tiles; fp32 x with a bf16 y: bf16 x takes either
  * y, fp32 x only an fp32 y); MOE_ERR_CUDA.  rows_cap = 0 launches nothing.  1 launch. */
 MOE_API moe_status_t moe_grouped_matmul(const moe_matmul_t* m, const int32_t* offsets, const void* x, const void* W,
                                         const void* bias, void* y, int32_t* status, cudaStream_t stream);
@@ -446,7 +447,8 @@ MOE_API moe_status_t moe_grouped_matmul(const moe_matmul_t* m, const int32_t* of
  * are in m->dtype; dW[E,K,N] and db[E,N] are fp32, contiguous, 16-byte aligned, and overwritten: an
  * expert without rows gets zeros.  out_dtype and transpose_w are not used (for a W[E,N,K] pass dy as x
  * and x as dy).  Sums run in a fixed order: the same inputs give the same bits.  Rows, offsets, status,
- * checks and errors as above; rows_cap = 0 writes zeros.  1 launch, 1 more with db. */
+ * checks and errors as above, and results must not overlap anything (dW or db = an input or each other is
+ * refused); rows_cap = 0 writes zeros.  1 launch, 1 more with db. */
 MOE_API moe_status_t moe_grouped_wgrad(const moe_matmul_t* m, const int32_t* offsets, const void* x, const void* dy,
                                        float* dW, float* db, int32_t* status, cudaStream_t stream);
 
@@ -476,7 +478,8 @@ typedef struct {
  * the same pitch; buffers must not overlap otherwise.  Any alignment that the type has is taken; 16-byte
  * aligned buffers with widths and pitches that 16 bytes divide run wide.  Errors: MOE_ERR_INVALID_ARG (null
  * or misaligned pointers, F < 1, rows_cap < 0, unknown type or activation, p outside [0, 1] or NaN, p > 0
- * without rng, a pitch below F, a result in place of an input with another pitch, du = dgate), MOE_ERR_UNSUPPORTED (rows_cap or F too large), MOE_ERR_CUDA.
+ * without rng, a pitch below F, a result in place of an input with another pitch, du = dgate),
+ * MOE_ERR_UNSUPPORTED (rows_cap or F too large), MOE_ERR_CUDA.
  * No workspace, no state: any number of calls at once.  1 launch; none for rows_cap = 0. */
 MOE_API moe_status_t moe_act_dropout(const moe_act_t* m, const void* u, const void* gate, void* y, cudaStream_t stream);
 MOE_API moe_status_t moe_act_dropout_backward(const moe_act_t* m, const void* dy, const void* u, const void* gate,
@@ -524,10 +527,11 @@ typedef struct {
  * offsets (clamped on the device, and recorded) and what is left unwritten are as in moe_grouped_matmul.
  * ws: a device buffer of moe_q4_workspace_size() bytes, 256-byte aligned, zero before its first use.  It holds
  * the error word for moe_get_device_status alone, so any number of calls may share one.  Sums run in a fixed order:
- * the same call gives the same bits on the same GPU.  Any number of rows is computed; the kernel is made for a few
- * (the weights are read once for every 16 rows of an expert).  Errors: MOE_ERR_INVALID_ARG (sizes and pointers as above; rows_cap < 0; a pitch below the row;
- * an unknown type or activation; x not 16-byte aligned, y, bias and offsets below their type's alignment; ws null
- * or misaligned), MOE_ERR_UNSUPPORTED (K not a multiple of group, ldx as above, fp32 x with a bf16 y, K or N above
+ * the same call gives the same bits on the same GPU.  y must not overlap the inputs.  Any number of rows is
+ * computed; the kernel is made for a few (the weights are read once for every 16 rows of an expert).
+ * Errors: MOE_ERR_INVALID_ARG (sizes and pointers as above; rows_cap < 0; a pitch below the row; an unknown type
+ * or activation; x not 16-byte aligned, y, bias and offsets below their type's alignment; y = an input; ws null or
+ * misaligned), MOE_ERR_UNSUPPORTED (K not a multiple of group, ldx as above, fp32 x with a bf16 y, K or N above
  * 2^24, a pitch of 2^31 or more, rows_cap >= 2^31 - 1024, more than 2^31 pieces of 16 rows and 32 columns, or
  * so many that an SM has 2^31 steps of 128 inputs),
  * MOE_ERR_WORKSPACE, MOE_ERR_CUDA.  1 launch; none for rows_cap = 0. */

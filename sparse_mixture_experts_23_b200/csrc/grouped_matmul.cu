@@ -640,6 +640,7 @@ moe_status_t check_matmul(const moe_matmul_t* m, bool wgrad, GroupedArgs* g) {
   const int step = bf16 ? 8 : 4;
   if (m->K % step != 0 || m->N % step != 0 || ldx % step != 0 || ldy % step != 0) return MOE_ERR_UNSUPPORTED;
   if (m->rows_cap >= (1LL << 31) - 1024) return MOE_ERR_UNSUPPORTED;  // row numbers past the last tile stay 32-bit
+  if (m->K > 1 << 30) return MOE_ERR_UNSUPPORTED;                     // as do steps past the last input
   // tile counters and grid sizes are 32-bit; a row pitch must fit a TMA stride (below 2^40 bytes)
   const long long mt = wgrad ? ((long long)m->K + 63) / 64 * m->E : m->rows_cap / 64 + m->E;
   const long long nt = ((long long)m->N + 63) / 64;
@@ -673,6 +674,7 @@ moe_status_t moe_grouped_matmul(const moe_matmul_t* m, const int32_t* offsets, c
   if (moe::misaligned(offsets, 4) || moe::misaligned(x, 16) || moe::misaligned(W, 16) || moe::misaligned(y, 16) ||
       moe::misaligned(bias, 16))
     return MOE_ERR_INVALID_ARG;
+  if (y == x || y == W || y == bias) return MOE_ERR_INVALID_ARG;  // other tiles still read what one has overwritten
   g.offsets = offsets;
   g.x = x;
   g.W = W;
@@ -704,6 +706,7 @@ moe_status_t moe_grouped_wgrad(const moe_matmul_t* m, const int32_t* offsets, co
   }
   if (offsets == nullptr || x == nullptr || dy == nullptr) return MOE_ERR_INVALID_ARG;
   if (moe::misaligned(offsets, 4) || moe::misaligned(x, 16) || moe::misaligned(dy, 16)) return MOE_ERR_INVALID_ARG;
+  if (dW == x || dW == dy || db == x || db == dy || db == dW) return MOE_ERR_INVALID_ARG;
   g.offsets = offsets;
   g.x = x;
   g.status = status;

@@ -744,6 +744,7 @@ moe_status_t moe_q4_matmul(const moe_q4_t* m, const int32_t* offsets, const void
   if (offsets == nullptr || x == nullptr || packed == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
   if (misaligned(offsets, 4) || misaligned(x, 16) || misaligned(packed, 16) || misaligned(bias, es) || misaligned(y, os))
     return MOE_ERR_INVALID_ARG;
+  if (y == x || y == packed || y == bias) return MOE_ERR_INVALID_ARG;  // other pieces still read what one has overwritten
   if (launch_q4_matmul(*m, offsets, x, packed, bias, y, static_cast<int32_t*>(ws), stream) != cudaSuccess)
     return MOE_ERR_CUDA;
   ++launch_count();

@@ -123,9 +123,9 @@ def grouped_matmul(x, W, offsets, bias=None, transpose_w: bool = False, out=None
     x ``[rows, K]`` (rows may be strided), W ``[E, K, N]`` -- or ``[E, N, K]`` with ``transpose_w``, which gives
     the data gradient ``dy @ W[e].T`` of a forward product -- bias ``[E, N]`` or None, all of one type (bf16 or
     f32); offsets int32 ``[E + 1]`` on the device.  ``out`` ``[rows, N]`` (rows may be strided) is made when not
-    given, of x's type or ``out_dtype``; rows past ``offsets[E]`` are not written.  bf16 wants K, N and row
-    pitches that are multiples of 8, f32 of 4.  ``status``: an int32 tensor, 0 at first, that a bad offset is
-    recorded in (see ``moe_get_device_status``)."""
+    given, of x's type or ``out_dtype``, and must not overlap the inputs; rows past ``offsets[E]`` are not
+    written.  bf16 wants K, N and row pitches that are multiples of 8, f32 of 4.  ``status``: an int32 tensor, 0 at
+    first, that a bad offset is recorded in (see ``moe_get_device_status``)."""
     index = x.get_device()
     code = _dtype(x, "x")
     ldx = _rows(x, "x", index)
@@ -305,9 +305,9 @@ def q4_matmul(x, W: Q4Weights, offsets, bias=None, activation=None, out=None, ou
 
     x ``[rows, K]`` bf16 or f32 (rows may be strided), W a ``Q4Weights``, bias ``[E, N]`` of x's type or None,
     activation "gelu", "silu" or None, ``out`` ``[rows, N]`` of x's type or ``out_dtype`` (f32 or x's; rows may be
-    strided); rows past ``offsets[E]`` are not written.  Made for a few rows an expert, right for any.  ws: a
-    ``q4_workspace()`` (made for the call when not given); a bad offset is recorded in its first word
-    (``moe_get_device_status(ws.data_ptr())``)."""
+    strided; must not overlap the inputs); rows past ``offsets[E]`` are not written.  Made for a few rows an expert,
+    right for any.  ws: a ``q4_workspace()`` (made for the call when not given); a bad offset is recorded in its first
+    word (``moe_get_device_status(ws.data_ptr())``)."""
     index = x.get_device()
     code = _dtype(x, "x")
     ldx = _rows(x, "x", index)

@@ -61,6 +61,21 @@ def test_matmul_types_and_pointers():
     assert moe.moe_last_launch_count() == 0
 
 
+def test_matmul_result_in_place_of_an_input():
+    OTHER, THIRD, FOURTH = FAKE + 4096, FAKE + 8192, FAKE + 12288
+    for bias, y in ((None, OTHER), (None, THIRD), (FOURTH, FOURTH)):
+        assert moe.moe_grouped_matmul(matmul(), FAKE, OTHER, THIRD, bias, y) == moe.MOE_ERR_INVALID_ARG
+    for dW, db in ((OTHER, None), (THIRD, None), (FOURTH, OTHER), (FOURTH, THIRD), (FOURTH, FOURTH)):
+        assert moe.moe_grouped_wgrad(matmul(), FAKE, OTHER, THIRD, dW, db) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_q4_matmul(q4(), FAKE, OTHER, THIRD, None, OTHER, FOURTH, WS) == moe.MOE_ERR_INVALID_ARG
+
+
+def test_matmul_of_too_many_inputs():
+    for dtype in (0, 1):
+        m = matmul(K=(1 << 30) + 8, ldx=(1 << 30) + 8, dtype=dtype, out_dtype=dtype)
+        assert moe.moe_grouped_matmul(m, FAKE, FAKE, FAKE, None, FAKE) == moe.MOE_ERR_UNSUPPORTED
+
+
 def test_matmul_struct_layout():
     assert ctypes.sizeof(moe.Matmul) == 56 and moe.Matmul.ldx.offset == 40 and moe.Matmul.K.offset == 16
 
