@@ -7,11 +7,11 @@
 // at counter (c / 4, r, offset, offset >> 32) under key (seed, seed >> 32) is at least p 2^32, and the
 // backward pass computes the same words again.  A dropped element is 0 whatever its inputs hold.
 //
-// Bound: issue slots next to HBM (4099 x 14336 gated bf16 forward and backward: 705 MB, 107 us at the copy rate).  A
-// vector of 16 bytes (8 bf16 or 4 fp32 columns: whole Philox blocks) of one row per thread and step, the next row's
+// Bound: issue slots next to HBM (4099 x 14336 gated bf16 forward and backward: 705 MB, 107 us at the copy rate; 940
+// MB and 143 us as the two calls that both read u and gate).  A vector of 16 bytes (8 bf16 or 4 fp32 columns: whole Philox blocks) of one row per thread and step, the next row's
 // vectors loaded before this one's arithmetic, 24 warps an SM that walk down the rows.  Ten Philox rounds are 20 wide
 // multiplies and 20 three-input xors for four elements; the round keys, the same for all elements, stay in registers.
-// Measured 162 us, 4.4 TB/s (298 us with two rows a thread and short-lived blocks; 174 us with 32 warps an SM, whose 64
+// Measured 162 us, 5.8 TB/s (298 us with two rows a thread and short-lived blocks; 174 us with 32 warps an SM, whose 64
 // registers a thread do not hold the keys).  24 and 36 instructions an element forward and backward, ALU pipe at 49%.
 // All arithmetic is fp32; each output is rounded once.
 #include <cuda_bf16.h>

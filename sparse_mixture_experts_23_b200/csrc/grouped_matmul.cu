@@ -81,8 +81,13 @@ constexpr int f32_smem(int fn, int groups) {
   return (steps > sums ? steps : sums);
 }
 
+// Blocks an SM holds at least (0: as the registers fall out).  Two of 4 groups, in 128 registers a thread, although a few
+// words then spill (1003 rows of 516 x 780 for 16 experts 60 -> 49 us).  Four of 2 groups would spill too and lose by it
+// (2500 rows of 712 x 1000 for 126 experts 262 and 271 us).
+constexpr int f32_blocks(int groups) { return groups == 4 ? 2 : 0; }
+
 template <int MODE, int FN, int KG>
-__global__ void __launch_bounds__(FN * KG) matmul_f32_kernel(F32Args a) {
+__global__ void __launch_bounds__(FN * KG, f32_blocks(KG)) matmul_f32_kernel(F32Args a) {
   constexpr int FT = FN, FB = FN + 4;  // threads of a group: 8 x 8 outputs each
   constexpr int kGroup = f32_group_floats(FN);
   __shared__ int offs[kMaxExperts + 1], prefix[kMaxExperts + 1];
@@ -543,7 +548,7 @@ cudaError_t launch_f32_groups(const F32Args& a, dim3 grid, cudaStream_t st) {
   return launch_parts(matmul_f32_kernel<MODE, FN, KG>, a, grid, FN * KG, smem, st);
 }
 // rows: about how many row tiles of the grid have work.  64 x 128 tiles where they fill the GPU twice over; else 64 x 64
-// ones with as many groups as let two blocks (of 4), four (of 2) or seven (of 1) of them share an SM.
+// ones with 8, 4 or 2 groups, as there are tiles for one, two or three blocks an SM.
 // k: how long the contraction is, about.
 template <int MODE>
 cudaError_t launch_f32(F32Args a, dim3 grid, long long rows, long long k, cudaStream_t st) {
