@@ -548,7 +548,8 @@ cudaError_t launch_f32_groups(const F32Args& a, dim3 grid, cudaStream_t st) {
   return launch_parts(matmul_f32_kernel<MODE, FN, KG>, a, grid, FN * KG, smem, st);
 }
 // rows: about how many row tiles of the grid have work.  64 x 128 tiles where they fill the GPU twice over; else 64 x 64
-// ones with 8, 4 or 2 groups, as there are tiles for one, two or three blocks an SM.
+// ones, with 8 groups where there is at most one tile an SM, 4 up to four of them (2000 rows of 2048 x 1024 for 4 experts,
+// 528 tiles: 224 us, 260 with 2 groups; 2400 of 1024 x 600 for 60, 670 tiles: 144 and 140), else 2.
 // k: how long the contraction is, about.
 template <int MODE>
 cudaError_t launch_f32(F32Args a, dim3 grid, long long rows, long long k, cudaStream_t st) {
@@ -559,7 +560,7 @@ cudaError_t launch_f32(F32Args a, dim3 grid, long long rows, long long k, cudaSt
     a.parts = f32_parts(tiles, k, 256);
     return launch_f32_groups<MODE, 64, 8>(a, grid, st);
   }
-  if (tiles <= 3 * sms) return launch_f32_groups<MODE, 64, 4>(a, grid, st);
+  if (tiles <= 4 * sms) return launch_f32_groups<MODE, 64, 4>(a, grid, st);
   return launch_f32_groups<MODE, 64, 2>(a, grid, st);
 }
 
