@@ -7,11 +7,13 @@ q = 2^-8 a rounding (u, gate, h, dh, du, dgate are rounded; |SiLU'| <= 1.1, |SiL
     du = m dh gate act'(u):  |m dh| (3 q |gate act'| + q |u gate| / 2)      dgate = m dh act(u):  |m dh| (2 q |act| + 1.1 q |u|)
     h = m act(u) gate:       |m| (2 q |act gate| + 1.1 q |u gate|)
 each times 1.02 for the products of two such errors and the fp32 sums, then through the magnitudes of the last product."""
+import threading
+
 import pytest
 import torch
 
 import sparse_mixture_experts_23_b200 as moe
-from oplib import randn
+from oplib import offsets_of, randn
 from philox import keep_mask
 
 pytestmark = pytest.mark.gpu
@@ -141,3 +143,57 @@ def test_training_step_of_gated_experts(dtype):
     g["x"].fill_(7.0)
     graph.replay()
     verify()
+
+
+def test_calls_at_once():
+    """The products, their gradients, the 4-bit product and the dropout from threads on streams of their own, and from two
+    graphs replayed side by side (one error word between them): the bits of one call after the other.  Few rows, few tiles
+    of a long contraction and long segments: every form that joins sums of several blocks is among them."""
+    sets = []
+    for i, (E, K, N, counts, dtype) in enumerate([
+            (4, 2048, 64, [3, 0, 9, 1], torch.bfloat16), (8, 512, 1024, [64] * 8, torch.bfloat16), (2, 4096, 200, [50, 42], torch.float32),
+            (1, 8192, 64, [10], torch.float32), (3, 64, 64, [3000, 1, 500], torch.float32), (1, 64, 520, [4000], torch.bfloat16)]):
+        n = sum(counts)
+        sets.append((randn((n, K), dtype, i), randn((E, K, N), dtype, i + 10), offsets_of(counts), randn((E, N), dtype, i + 20),
+                     randn((n, N), dtype, i + 30)))
+    q = moe.Q4Weights(*moe.q4_quantize(randn((4, 1024, 512), torch.float32, 50), group=64))
+    ws, xq, oq = moe.q4_workspace(), randn((30, 1024), torch.bfloat16, 51), offsets_of([7, 0, 20, 3])
+    rng = torch.tensor([3, 4], device="cuda")
+
+    def work():
+        r = [moe.q4_matmul(xq, q, oq, ws=ws), moe.act_dropout(sets[1][4], p=0.3, rng=rng)]
+        for x, W, offsets, bias, dy in sets:
+            r += [moe.grouped_matmul(x, W, offsets, bias), moe.grouped_matmul(dy, W, offsets, transpose_w=True)]
+            r += moe.grouped_wgrad(x, dy, offsets, bias_grad=True)
+        return r
+
+    want = work()
+    torch.cuda.synchronize()
+    same = []
+
+    def one():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(5):
+                got = work()
+                stream.synchronize()
+                same.append(all(map(torch.equal, got, want)))
+
+    threads = [threading.Thread(target=one) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert same == [True] * 15
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = work()
+        graphs.append((g, got, torch.cuda.Stream()))
+    for _ in range(5):
+        for g, _, stream in graphs:
+            with torch.cuda.stream(stream):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(all(map(torch.equal, got, want)) for _, got, _ in graphs) and moe.moe_get_device_status(ws.data_ptr()) == 0
