@@ -418,7 +418,7 @@ typedef struct {
   int32_t K;             /* contraction of the forward product */
   int32_t N;             /* output columns of the forward product */
   moe_dtype_t dtype;     /* storage type of x, W, bias (and of dy) */
-  moe_dtype_t out_dtype; /* storage type of y; the products are summed in fp32 and rounded once */
+  moe_dtype_t out_dtype; /* storage type of y; sums are fp32 (see below), rounded once at the end */
   int32_t transpose_w;   /* 0: W[E,K,N] (the layout of W1 and W2); 1: W[E,N,K] */
   int64_t ldx;           /* elements between rows of x; 0 = K (contiguous) */
   int64_t ldy;           /* elements between rows of y (dy); 0 = N */
@@ -432,8 +432,9 @@ typedef struct {
  * or written, and recorded in status.  Rows of y in [offsets[E], rows_cap), and columns [N, ldy), are
  * left as they were.  status: an optional (NULL) device int32, 4-byte aligned and 0 before its first
  * use, where a bad offset or a bounded wait that ran out is recorded for moe_get_device_status.
- * bf16: tcgen05 tensor cores; fp32: CUDA cores.  Sums run in an order that sizes, types and the GPU fix:
- * the same call gives the same bits.
+ * bf16: tcgen05 tensor cores, whose fp32 sums cut where CUDA cores round; every 768 inputs are one such sum, and
+ * those are added in fp32 (about 7e-7 of the magnitudes, at any K and for either y).  fp32: CUDA cores.  Sums run in
+ * an order that sizes, types and the GPU fix: the same call gives the same bits.
  * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers - 16 bytes, offsets and status 4 - E
  * outside [1, 256], rows_cap < 0, K or N < 1, ld below the row length, unknown types, y = x, W or bias);
  * MOE_ERR_UNSUPPORTED (bf16: K, N, ldx or ldy not a multiple of 8; fp32: of 4; rows_cap

@@ -9,7 +9,7 @@
 //   GEMM2 (EPI_COMBINE):  out[t, n] += w(t,s) * ( sum_k h[r,k] W2[e,k,n] + b2[e,n] ),  t,s = row r's
 //   GEMM2 (EPI_STORE_Y):  y[r, n]   = sum_k h[r,k] W2[e,k,n] + b2[e,n]
 //   moe_grouped_matmul (EPI_ROWS_F32, EPI_ROWS_BF16): the same sum with any N and K that are multiples of 8, rows of
-//   x and y at a pitch of their own, and caller-given offsets
+//   x and y at a pitch of their own, caller-given offsets, and every kSumK inputs summed apart
 //
 // Design (one persistent CTA per SM, 64 + 32 * kEpiWarps threads: 192 with the default 4 epilogue warps):
 //   warp 0      TMA producer: A tile [128 rows x 64 k] (K-major, 128B swizzle) and B tile
@@ -70,6 +70,15 @@ enum {
 __host__ __device__ constexpr bool epi_h(int epi) { return epi == EPI_GELU || epi == EPI_SILU; }
 __host__ __device__ constexpr bool epi_rows(int epi) { return epi == EPI_ROWS_F32 || epi == EPI_ROWS_BF16; }
 __host__ __device__ constexpr bool epi_dgrad(int epi) { return epi == EPI_DGRAD_GELU || epi == EPI_DGRAD_SILU; }
+// Inputs of a tensor-core sum of the row epilogues.  The tensor core cuts where it adds, a little towards zero at each of
+// its steps of 16: one sum over 14336 inputs is 1.6e-5 off its result, 6.4e-5 where the terms have one sign, and a bf16
+// y's rounding goes the other way for 0.8% to 1.3% of the results.  So the accumulator of every kSumK inputs is a sum of
+// its own, which the epilogue adds into fp32 registers, in order: 7e-7 at any length (the layer's own GEMMs keep one sum).
+// What it costs: nothing to 1% on whole tiles, 0.4 to 1 us of 11 to 18 where a cluster shares K.
+constexpr int kSumK = 768;
+// Up to 128 columns a thread are held there: two warps a lane quarter for tiles of 256.
+__host__ __device__ constexpr int epi_warps(int epi, int bn) { return epi_rows(epi) && bn == 256 ? 8 : kEpiWarps; }
+__host__ __device__ constexpr int gemm_threads(int epi, int bn) { return 64 + 32 * epi_warps(epi, bn); }
 
 template <int BN>
 struct Cfg {
@@ -222,7 +231,7 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const uint32_t
     mine[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
                           __uint_as_float(r[4 * q + 3]));
   __syncwarp();
-  const float bj = brow && (EPI != EPI_ROWS_F32 || n0 + lane < g.N) ? __bfloat162float(brow[n0 + lane]) : 0.f;
+  const float bj = brow ? __bfloat162float(brow[n0 + lane]) : 0.f;
   const int nr = nrows < 32 ? nrows : 32;
   // 8 rows at a time: their values (and activations) are independent, so the latency of one row's
   // chain overlaps the others' (one warp per SM sub-partition runs this loop)
@@ -247,8 +256,6 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const uint32_t
         const int tok = __shfl_sync(0xffffffffu, my_tok, i);
         const float w = __shfl_sync(0xffffffffu, my_w, i);
         if (ok) atomicAdd(g.out + (size_t)tok * g.N + n0 + lane, w * v[q]);
-      } else if (EPI == EPI_ROWS_F32) {
-        if (ok && n0 + lane < g.N) g.y[(size_t)(grow0 + off) * g.ldo + n0 + lane] = v[q];
       } else {
         if (ok) g.y[(size_t)(grow0 + off) * g.N + n0 + lane] = v[q];
       }
@@ -323,51 +330,111 @@ __device__ __forceinline__ void epilogue_h_rows(const GemmArgs& g, const uint32_
   }
 }
 
-// EPI_ROWS_BF16: a 64-column group of a warp's 32 rows (lane i owns tile row i), y = bf16(acc + bias).  The
-// values pass through the warp's staging box in the same swizzle (16-byte piece j of row i at j ^ (i % 8):
-// writes and reads are free of bank conflicts), so that 8 lanes store one row's 128 contiguous bytes.  Row i
-// is output row grow0 + off_i as in epilogue_chunk; rows past the segment and columns past N (multiples of
-// 8: whole pieces) are skipped.  The rounding to bf16 is the output type's own, once, after the bias, whose 8 pieces of
-// these columns are at `bias` in shared memory (rows_bias) or absent.  On tiles of a short K this epilogue sets the pace.
-// The bias of a tile's up to 256 columns, 16 bytes a lane, into the kilobyte behind the warp's staging box: loaded before
-// the wait for the accumulator, in place of 8 loads behind it for every 64 columns.
+// The row epilogues: y = sum + bias for 32 columns of a warp's 32 rows (lane i owns tile row i).  The values pass through
+// the warp's staging box, 64-byte rows with 16-byte piece j of row i at j ^ (i / 2 % 4) (writes and reads are free of bank
+// conflicts), so that 4 lanes store one row's 64 contiguous bytes.  Row i is output row grow0 + gap * (i / 8) + i % 8 (gap 8,
+// or 32 where rows are spread); rows past the segment and columns past N (multiples of 8: whole pieces) are skipped.
+constexpr int kRowsBox = 2048;  // of a warp; its bias pieces lie behind
+static_assert(kRowsBox + 256 <= kStgWarpBytes / 2, "a box and 128 bf16 of bias for each of 8 warps");
+
+// The bias of a warp's up to 128 columns, 16 bytes a lane, behind the warp's staging box: loaded before the wait for the
+// accumulator, since on tiles of a short K the epilogue sets the pace.
 __device__ __forceinline__ const uint4* rows_bias(uint8_t* stg, const __nv_bfloat16* brow, int n0, int cols, int N, int lane) {
   if (brow == nullptr) return nullptr;
-  uint4* to = reinterpret_cast<uint4*>(stg + 4096);
+  uint4* to = reinterpret_cast<uint4*>(stg + kRowsBox);
   if (8 * lane < cols) to[lane] = n0 + 8 * lane < N ? bias8(brow, n0 + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
   __syncwarp();
   return to;
 }
-template <bool SPREAD>
-__device__ __forceinline__ void epilogue_rows_bf16(const GemmArgs& g, const uint32_t (&r0)[32], const uint32_t (&r1)[32],
-                                                   uint8_t* stg, int lane, int grow0, int nrows, const uint4* bias, int n0) {
-  uint8_t* row = stg + lane * 128;
+
+// EPI_ROWS_BF16.  The rounding to bf16 is the output type's own, once, after the bias, whose 4 pieces of these columns are
+// at `bias` in shared memory (rows_bias) or absent.
+__device__ __forceinline__ void epilogue_rows_bf16(const GemmArgs& g, const float (&r)[32], uint8_t* stg, int lane, int grow0,
+                                                   int nrows, int gap, const uint4* bias, int n0) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t* src = j < 4 ? &r0[8 * j] : &r1[8 * (j - 4)];
+  for (int j = 0; j < 4; ++j) {
     const uint4 bb = bias ? bias[j] : make_uint4(0u, 0u, 0u, 0u);
     const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&bb);
     uint32_t w[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const float2 f = __bfloat1622float2(b2[u]);
-      const __nv_bfloat162 v =
-          __floats2bfloat162_rn(__uint_as_float(src[2 * u]) + f.x, __uint_as_float(src[2 * u + 1]) + f.y);
+      const __nv_bfloat162 v = __floats2bfloat162_rn(r[8 * j + 2 * u] + f.x, r[8 * j + 2 * u + 1] + f.y);
       w[u] = *reinterpret_cast<const uint32_t*>(&v);
     }
-    *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(stg + lane * 64 + ((j ^ (lane >> 1 & 3)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncwarp();
-  const int piece = lane & 7, n = n0 + 8 * piece;
+  const int piece = lane & 3, n = n0 + 8 * piece;
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int i = 4 * p + (lane >> 3);
-    const int off = SPREAD ? 32 * (i >> 3) + (i & 7) : i;
-    if ((SPREAD ? 32 * (p >> 1) + 4 * (p & 1) : 4 * p) >= nrows) break;  // the group's first row: no later group has any
-    const uint4 v = *reinterpret_cast<const uint4*>(stg + i * 128 + ((piece ^ (i & 7)) * 16));
+  for (int p = 0; p < 4; ++p) {
+    const int i = 8 * p + (lane >> 2), first = gap * p, off = first + (lane >> 2);
+    if (first >= nrows) break;  // no later group has a row
+    const uint4 v = *reinterpret_cast<const uint4*>(stg + i * 64 + ((piece ^ (i >> 1 & 3)) * 16));
     if (off < nrows && n < g.N) *reinterpret_cast<uint4*>(g.h_out + (size_t)(grow0 + off) * g.ldo + n) = v;
   }
   __syncwarp();
+}
+
+// EPI_ROWS_F32, sixteen columns at a time.  bias: of the first of them, or null.
+__device__ __forceinline__ void epilogue_rows_f32(const GemmArgs& g, const float (&r)[32], uint8_t* stg, int lane, int grow0,
+                                                  int nrows, int gap, const uint4* bias, int n0) {
+  const int piece = lane & 3;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<float4*>(stg + lane * 64 + ((j ^ (lane >> 1 & 3)) * 16)) =
+          make_float4(r[16 * h + 4 * j], r[16 * h + 4 * j + 1], r[16 * h + 4 * j + 2], r[16 * h + 4 * j + 3]);
+    __syncwarp();
+    const int n = n0 + 16 * h + 4 * piece;
+    const uint2 b = bias ? reinterpret_cast<const uint2*>(bias)[4 * h + piece] : make_uint2(0u, 0u);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int i = 8 * p + (lane >> 2), first = gap * p, off = first + (lane >> 2);
+      if (first >= nrows) break;  // no later group has a row
+      float4 v = *reinterpret_cast<const float4*>(stg + i * 64 + ((piece ^ (i >> 1 & 3)) * 16));
+      v.x += __uint_as_float(b.x << 16);
+      v.y += __uint_as_float(b.x & 0xffff0000u);
+      v.z += __uint_as_float(b.y << 16);
+      v.w += __uint_as_float(b.y & 0xffff0000u);
+      if (off < nrows && n < g.N) *reinterpret_cast<float4*>(g.y + (size_t)(grow0 + off) * g.ldo + n) = v;
+    }
+    __syncwarp();
+  }
+}
+
+template <int EPI>
+__device__ __forceinline__ void epilogue_rows(const GemmArgs& g, const float (&r)[32], uint8_t* stg, int lane, int grow0, int nrows,
+                                              int gap, const uint4* bias, int n0) {
+  if constexpr (EPI == EPI_ROWS_BF16) epilogue_rows_bf16(g, r, stg, lane, grow0, nrows, gap, bias, n0);
+  else epilogue_rows_f32(g, r, stg, lane, grow0, nrows, gap, bias, n0);
+}
+
+// Adds one part of a tile's sums: Q chunks of 32 accumulator columns from `taddr` on.  n0: the first chunk's output column;
+// chunks past N, and all but `chunks`, are left out.  With 4 chunks, 16 columns at a time: more would not fit the registers
+// of a 256-wide tile's warps beside the sums (taking the first part straight into the sums spills too: 27 -> 31 us for 21
+// experts, 1001 rows, 176 x 7592).
+template <int Q>
+__device__ __forceinline__ void add_part(float (&sum)[Q][32], uint32_t taddr, int n0, int N, int chunks) {
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (q >= chunks || n0 + 32 * q >= N) continue;
+    if constexpr (Q <= 2) {
+      uint32_t r[32];
+      tmem_ld32(taddr + 32 * q, r);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) sum[q][j] += __uint_as_float(r[j]);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 32; h += 16) {
+        uint32_t r[16];
+        tmem_ld16(taddr + 32 * q + h, r);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum[q][h + j] += __uint_as_float(r[j]);
+      }
+    }
+  }
 }
 
 // Backward epilogue of 32 accumulator columns of one row (lane = row): G = acc is the row's
@@ -536,10 +603,12 @@ __device__ __forceinline__ void router_epilogue(const GemmArgs& g, uint32_t tadd
 // range; then every CTA collects its share of the tile's columns from all of them through distributed shared memory
 // (the stage ring is free by then), adds them in rank order and stores them.
 template <int BN, int EPI, bool BKM, bool KSPLIT = false>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(gemm_threads(EPI, BN), 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmA16, GemmArgs g) {
   using C = Cfg<BN>;
+  constexpr bool PARTS = epi_rows(EPI);  // a sum of its own every kSumK inputs
+  constexpr int kPart = kSumK / BK, EW = epi_warps(EPI, BN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -556,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = g.E, NT = (g.N + BN - 1) / BN, KB = (g.K + BK - 1) / BK;
-  float* stg = reinterpret_cast<float*>(smem + C::kStgOff + (warp >= 2 ? warp - 2 : 0) * kStgWarpBytes);
+  float* stg = reinterpret_cast<float*>(smem + C::kStgOff + (warp >= 2 ? warp - 2 : 0) * (kEpiWarps * kStgWarpBytes / EW));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -565,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), kEpiWarps);
+      mbar_init(tempty_bar(b), EW);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -577,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (epi_rows(EPI)) {
     if (warp == 0) load_segments(g.offsets, E, g.rows_cap, BM, NT, offs, prefix, g.status, blockIdx.x == 0);
   } else {
-    for (int i = threadIdx.x; i <= E; i += kThreads) offs[i] = g.offsets ? g.offsets[i] : (i == 0 ? 0 : g.single_rows);
+    for (int i = threadIdx.x; i <= E; i += (int)blockDim.x) offs[i] = g.offsets ? g.offsets[i] : (i == 0 ? 0 : g.single_rows);
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
   __syncthreads();
@@ -596,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // work items: every tile, or every (tile, K part) with split K
   const int KS = g.k_splits > 1 ? g.k_splits : 1;
   const int total = prefix[E] * KS;
-  bool summed = false;  // KSPLIT: this CTA's accumulator is there
+  bool summed = false;  // KSPLIT: this CTA's sums are there
+  float ksum[KSPLIT ? BN / 32 : 1][32] = {};
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer -----------------
@@ -665,16 +735,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       bool issued = false;
       for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, ++it) {
-        const int buf = it & 1;
+        int buf = it & 1;
         const uint32_t tphase = (uint32_t)((it >> 1) & 1);
         if (!mbar_wait(tempty_bar(buf), tphase ^ 1u, g.wait_limit, abort_flag, g.status, kDevTimeoutMma)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN);
+        uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN);
         const int kb0 = KB * (tile % KS) / KS, kb1 = KB * (tile % KS + 1) / KS;
+        int part0 = kb0;
         for (int kb = kb0; kb < kb1; ++kb) {
+          if (PARTS && kb - part0 == kPart) {
+            // hand this part's sums to the epilogue and go on in the other accumulator
+            mma_commit(tfull_bar(buf));
+            part0 = kb;
+            ++it;
+            buf = it & 1;
+            if (!mbar_wait(tempty_bar(buf), (uint32_t)((it >> 1) & 1) ^ 1u, g.wait_limit, abort_flag, g.status, kDevTimeoutMma)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            d_tmem = tmem_base + (uint32_t)(buf * BN);
+          }
           if (!mbar_wait(full_bar(stage), phase, g.wait_limit, abort_flag, g.status, kDevTimeoutMma)) {
             ok = false;
             break;
@@ -688,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)  // 16 k: 32 bytes of a K-major operand, 16 rows of an MN-major one
             mma_bf16(d_tmem, a_lo + kk * 2, a_hi, b_lo + kk * (BKM ? 2 : 128), b_hi, BKM ? (C::kIdesc & ~(1u << 16)) : C::kIdesc,
-                     kk != 0 || kb != kb0 ? 1u : 0u);
+                     kk != 0 || kb != part0 ? 1u : 0u);
           issued = true;
           mma_commit(empty_bar(stage));
           if (++stage == C::kStages) {
@@ -720,17 +804,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       decode_tile(tile / KS, prefix, offs, E, NT, e, m_local, n_idx, row0, rows);
       const int buf = it & 1;
       const uint32_t tphase = (uint32_t)((it >> 1) & 1);
-      const uint4* rbias = nullptr;
-      if constexpr (EPI == EPI_ROWS_BF16 && !KSPLIT)
-        rbias = rows_bias(reinterpret_cast<uint8_t*>(stg), g.bias ? g.bias + (size_t)e * g.N : nullptr, n_idx * BN, BN, g.N, lane);
+      if constexpr (PARTS) {
+        constexpr int Q = BN / 32 / (EW / 4);  // 32-column chunks of this warp
+        const int kparts = (KB * (tile % KS + 1) / KS - KB * (tile % KS) / KS + kPart - 1) / kPart;
+        const int n0 = n_idx * BN + half * Q * 32;
+        uint8_t* box = reinterpret_cast<uint8_t*>(stg);
+        const uint4* bias = KSPLIT ? nullptr : rows_bias(box, g.bias ? g.bias + (size_t)e * g.N : nullptr, n0, Q * 32, g.N, lane);
+        float sum[Q][32] = {};
+        bool got = true;
+        for (int p = 0; p < kparts; ++p) {
+          const int b = (it + p) & 1;
+          got = __all_sync(0xffffffffu, mbar_wait(tfull_bar(b), (uint32_t)(((it + p) >> 1) & 1), g.wait_limit, abort_flag, g.status,
+                                                  kDevTimeoutEpilogue));
+          if (!got) break;
+          tc_fence_after();
+          const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * BN + half * Q * 32);
+          if constexpr (KSPLIT) add_part(ksum, taddr, 0, BN, Q);  // columns past N too: every share is sent
+          else add_part(sum, taddr, n0, g.N, Q);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty_bar(b));
+        }
+        if (!got) break;
+        if constexpr (KSPLIT) {
+          summed = true;
+          break;
+        }
+        it += kparts - 1;
+        const int wrows = rows - wbase;  // > 0: some of this warp's 32 rows lie inside the segment
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          if (wrows <= 0 || n0 + 32 * q >= g.N) continue;
+          epilogue_rows<EPI>(g, sum[q], box, lane, row0 + wbase, wrows, spread ? 32 : 8, bias ? bias + 4 * q : nullptr, n0 + 32 * q);
+        }
+        continue;
+      }
       // every lane waits; the warp leaves together if any lane gave up (tcgen05.ld is warp-wide)
       const bool got = mbar_wait(tfull_bar(buf), tphase, g.wait_limit, abort_flag, g.status, kDevTimeoutEpilogue);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
-      if constexpr (KSPLIT) {
-        summed = true;
-        break;
-      }
       const bool row_ok = r_in_tile < rows;
       const int grow = row0 + r_in_tile;
       float wgt = 0.f;
@@ -749,24 +861,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (half == 0 && wrows > 0)
           router_epilogue<BN>(g, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN), stg, lane,
                               row0 + quarter * 32, wrows);
-      } else if constexpr (EPI == EPI_ROWS_BF16) {
-#pragma unroll 1
-        for (int c = half * kChunks; c < (half + 1) * kChunks; c += 2) {
-          const int n0 = n_idx * BN + c * 32;
-          if (wrows <= 0 || n0 >= g.N) break;
-          uint32_t r0[32], r1[32];
-          const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN + c * 32);
-          tmem_ld32_start(taddr, r0);
-          tmem_ld32_start(taddr + 32, r1);
-          tmem_wait_ld(r0, r1);
-          const uint4* b8 = rbias ? rbias + c * 4 : nullptr;
-          if (spread) epilogue_rows_bf16<true>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, row0 + wbase, wrows, b8, n0);
-          else epilogue_rows_bf16<false>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, row0 + wbase, wrows, b8, n0);
-        }
       } else
 #pragma unroll 1
       for (int c = half * kChunks; c < (half + 1) * kChunks; ++c) {
-        if (epi_rows(EPI) && n_idx * BN + c * 32 >= g.N) break;
         uint32_t r[32];
         tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN + c * 32), r);
         if constexpr (epi_dgrad(EPI)) {
@@ -792,20 +889,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (KSPLIT) {
     __syncwarp();
     static_assert(kEpiWarps == 4 && epi_rows(EPI), "one epilogue warp for each lane quarter");
-    const int W = BN / KS;  // columns of a CTA's share
+    const int W = BN / KS, shift = __ffs(W) - 1;  // columns of a CTA's share, a power of two
     const int rank = (int)cluster_ctarank(), row = (warp & 3) * 32 + lane;
     cluster_sync_all();  // every CTA's MMAs have read their stages
     if (warp >= 2 && summed) {
-#pragma unroll 1
+#pragma unroll
       for (int c = 0; c < BN / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(c * 32), r);
+        const float(&r)[32] = ksum[c];
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
           const int col = c * 32 + j;
-          const uint32_t to = peer_addr(sbase + (uint32_t)(((rank * BM + row) * W + col % W) * 4), (uint32_t)(col / W));
-          asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(r[j]), "r"(r[j + 1]), "r"(r[j + 2]),
-                       "r"(r[j + 3])
+          const uint32_t to = peer_addr(sbase + (uint32_t)(((rank * BM + row) * W + (col & (W - 1))) * 4), (uint32_t)(col >> shift));
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "f"(r[j]), "f"(r[j + 1]), "f"(r[j + 2]),
+                       "f"(r[j + 3])
                        : "memory");
         }
       }
@@ -913,10 +1009,12 @@ __device__ __forceinline__ void decode_tile_m(int tile, const int* prefix, const
 }
 
 template <int EPI, bool BKM>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(EPI, PairCfg::kTileN), 1)
     grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                              const __grid_constant__ CUtensorMap tmC, GemmArgs g) {
   using C = PairCfg;
+  constexpr bool PARTS = epi_rows(EPI);  // a sum of its own every kSumK inputs
+  constexpr int kPart = kSumK / C::kStageK, EW = epi_warps(EPI, C::kTileN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -932,7 +1030,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int* prefix = offs + 260;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* stg = reinterpret_cast<float*>(smem + C::kStgOff + (warp >= 2 ? warp - 2 : 0) * kStgWarpBytes);
+  float* stg = reinterpret_cast<float*>(smem + C::kStgOff + (warp >= 2 ? warp - 2 : 0) * (kEpiWarps * kStgWarpBytes / EW));
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
@@ -945,7 +1043,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), 2 * kEpiWarps);  // every epilogue warp of both CTAs of the pair
+      mbar_init(tempty_bar(b), 2 * EW);  // every epilogue warp of both CTAs of the pair
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -956,7 +1054,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if constexpr (epi_rows(EPI)) {
     if (warp == 0) load_segments(g.offsets, E, g.rows_cap, C::kTileM, NT, offs, prefix, g.status, blockIdx.x == 0);
   } else {
-    for (int i = threadIdx.x; i <= E; i += kThreads) offs[i] = g.offsets[i];
+    for (int i = threadIdx.x; i <= E; i += (int)blockDim.x) offs[i] = g.offsets[i];
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), C::kTmemCols);
   __syncthreads();
@@ -1035,7 +1133,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       bool issued = false;
       for (int tile = cluster_id; tile < total && ok; tile += nclusters, ++it) {
-        const int buf = it & 1;
+        int buf = it & 1, part0 = 0;
         const uint32_t tphase = (uint32_t)((it >> 1) & 1);
         int e_, m_l, n_i, r0_, rows;
         decode_tile_m(tile, prefix, offs, E, NT, C::kTileM, e_, m_l, n_i, r0_, rows);
@@ -1046,8 +1144,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * C::kTileN);
+        uint32_t d_tmem = tmem_base + (uint32_t)(buf * C::kTileN);
         for (int kb = 0; kb < KB; ++kb) {
+          if (PARTS && kb - part0 == kPart) {
+            // hand this part's sums to the epilogue and go on in the other accumulator
+            mma_commit_both(tfull_bar(buf));
+            part0 = kb;
+            ++it;
+            buf = it & 1;
+            if (!mbar_wait(tempty_bar(buf), (uint32_t)((it >> 1) & 1) ^ 1u, g.wait_limit, abort_flag, g.status, kDevTimeoutMma)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            d_tmem = tmem_base + (uint32_t)(buf * C::kTileN);
+          }
           if (!mbar_wait(full_bar(stage), phase, g.wait_limit, abort_flag, g.status, kDevTimeoutMma)) {
             ok = false;
             break;
@@ -1062,7 +1173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < C::kStageK / 16; ++kk) {
             const int sk = kk / (BK / 16), ks = kk % (BK / 16);
             mma_bf16_pair(d_tmem, a_lo + sk * (C::kASubBytes / 16) + ks * 2, a_hi,
-                          b_lo + sk * (C::kBSubBytes / 16) + ks * (BKM ? 2 : 128), b_hi, idesc, kk != 0 || kb != 0 ? 1u : 0u);
+                          b_lo + sk * (C::kBSubBytes / 16) + ks * (BKM ? 2 : 128), b_hi, idesc, kk != 0 || kb != part0 ? 1u : 0u);
           }
           issued = true;
           mma_commit_both(empty_bar(stage));  // frees this stage in both CTAs once its MMAs are done
@@ -1095,13 +1206,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       decode_tile_m(tile, prefix, offs, E, NT, C::kTileM, e, m_local, n_idx, row0, rows);
       const int buf = it & 1;
       const uint32_t tphase = (uint32_t)((it >> 1) & 1);
-      const uint4* rbias = nullptr;
-      if constexpr (EPI == EPI_ROWS_BF16)
-        rbias = rows_bias(reinterpret_cast<uint8_t*>(stg), g.bias ? g.bias + (size_t)e * g.N : nullptr, n_idx * C::kTileN, C::kTileN,
-                          g.N, lane);
-      const bool got = mbar_wait(tfull_bar(buf), tphase, g.wait_limit, abort_flag, g.status, kDevTimeoutEpilogue);
-      if (!__all_sync(0xffffffffu, got)) break;
-      tc_fence_after();
+      if constexpr (!PARTS) {
+        const bool got = mbar_wait(tfull_bar(buf), tphase, g.wait_limit, abort_flag, g.status, kDevTimeoutEpilogue);
+        if (!__all_sync(0xffffffffu, got)) break;
+        tc_fence_after();
+      }
       // Full tile: this CTA's 128 rows in TMEM lanes 0..127, 256 columns.  Half tile (M = 128 over the
       // pair): this CTA's 64 rows x 256 columns sit in 128 TMEM columns, lanes 0..63 holding columns
       // 0..127 and lanes 64..127 columns 128..255 -- so lane quarter q has rows 32*(q%2).. and
@@ -1123,9 +1232,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const __nv_bfloat16* brow = g.bias ? g.bias + (size_t)e * g.N : nullptr;
       const int wrows = my_rows - qr * 32;  // rows of this warp's 32 that lie inside the segment
       const int wrow0 = row0 + cta_rows * (int)rank + qr * 32;
-      const int nch = (hm ? C::kTileN / 64 : C::kTileN / 32) / (kEpiWarps / 4);  // 32-column chunks per warp
+      const int nch = (hm ? C::kTileN / 64 : C::kTileN / 32) / (EW / 4);  // 32-column chunks per warp
       const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * C::kTileN);
-      if constexpr (epi_h(EPI)) {
+      if constexpr (PARTS) {
+        constexpr int Q = C::kTileN / 32 / (EW / 4);
+        const int kparts = (KB + kPart - 1) / kPart, n0 = n_idx * C::kTileN + colbase + half * nch * 32;
+        uint8_t* box = reinterpret_cast<uint8_t*>(stg);
+        const uint4* bias = rows_bias(box, brow, n0, nch * 32, g.N, lane);
+        float sum[Q][32] = {};
+        bool got = true;
+        for (int p = 0; p < kparts; ++p) {
+          const int b = (it + p) & 1;
+          got = __all_sync(0xffffffffu, mbar_wait(tfull_bar(b), (uint32_t)(((it + p) >> 1) & 1), g.wait_limit, abort_flag, g.status,
+                                                  kDevTimeoutEpilogue));
+          if (!got) break;
+          tc_fence_after();
+          add_part(sum, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * C::kTileN + half * nch * 32), n0, g.N, nch);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(b ? tempty_leader1 : tempty_leader0);
+        }
+        if (!got) break;
+        it += kparts - 1;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          if (q >= nch || wrows <= 0 || n0 + 32 * q >= g.N) continue;
+          epilogue_rows<EPI>(g, sum[q], box, lane, wrow0, wrows, 8, bias ? bias + 4 * q : nullptr, n0 + 32 * q);
+        }
+        continue;
+      } else if constexpr (epi_h(EPI)) {
 #pragma unroll 1
         for (int c = half * nch; c < (half + 1) * nch; c += 2) {
           uint32_t r0[32], r1[32];
@@ -1135,18 +1270,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (wrows >= 32)
             epilogue_h_box<EPI>(&tmC, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, brow, n0, wrow0, g.u_out, g.N);
           else if (wrows > 0) epilogue_h_rows<EPI>(g, r0, r1, lane, wrows, brow, n0, wrow0);
-        }
-      } else if constexpr (EPI == EPI_ROWS_BF16) {
-#pragma unroll 1
-        for (int c = half * nch; c < (half + 1) * nch; c += 2) {
-          const int n0 = n_idx * C::kTileN + colbase + c * 32;
-          if (wrows <= 0 || n0 >= g.N) break;
-          uint32_t r0[32], r1[32];
-          tmem_ld32_start(taddr + c * 32, r0);
-          tmem_ld32_start(taddr + (c + 1) * 32, r1);
-          tmem_wait_ld(r0, r1);
-          epilogue_rows_bf16<false>(g, r0, r1, reinterpret_cast<uint8_t*>(stg), lane, wrow0, wrows,
-                                    rbias ? rbias + (colbase + c * 32) / 8 : nullptr, n0);
         }
       } else if constexpr (epi_dgrad(EPI)) {
         float dw = 0.f;
@@ -1160,7 +1283,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
 #pragma unroll 1
         for (int c = half * nch; c < (half + 1) * nch; ++c) {
-          if (epi_rows(EPI) && n_idx * C::kTileN + colbase + c * 32 >= g.N) break;
           uint32_t r[32];
           tmem_ld32(taddr + c * 32, r);
           if (wrows > 0)
@@ -1937,7 +2059,7 @@ cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const GemmA
   auto kern = grouped_gemm_kernel<BN, EPI, BKM>;
   cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kern), Cfg<BN>::kSmemBytes);
   if (err != cudaSuccess) return err;
-  kern<<<grid, kThreads, Cfg<BN>::kSmemBytes, st>>>(ma, mb, ma16 ? *ma16 : ma, g);
+  kern<<<grid, gemm_threads(EPI, BN), Cfg<BN>::kSmemBytes, st>>>(ma, mb, ma16 ? *ma16 : ma, g);
   return cudaGetLastError();
 }
 
@@ -1947,7 +2069,7 @@ cudaError_t launch_pair(const CUtensorMap& ma, const CUtensorMap& mb, const CUte
   auto kern = grouped_gemm_pair_kernel<EPI, BKM>;
   cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kern), PairCfg::kSmemBytes);
   if (err != cudaSuccess) return err;
-  kern<<<grid & ~1, kThreads, PairCfg::kSmemBytes, st>>>(ma, mb, mc, g);
+  kern<<<grid & ~1, gemm_threads(EPI, PairCfg::kTileN), PairCfg::kSmemBytes, st>>>(ma, mb, mc, g);
   return cudaGetLastError();
 }
 

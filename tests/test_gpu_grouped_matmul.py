@@ -265,3 +265,28 @@ def test_few_tiles_of_a_long_contraction(counts, K, N, trans):
     """K shared by the CTAs of a cluster, in 2, 4 or 8 parts."""
     check_forward(counts, K, N, BF, BF, trans, bias=N != 64, pad=1, spare=40)
     check_forward(counts, K, N, BF, F32, trans, bias=N != 72, spare=3, seed=4)
+
+
+# every form of the bf16 product: K shared by a cluster, 64-wide tiles, 128 and 256 with spread rows, 256 with 16-row boxes,
+# pair tiles (full and half)
+LONG = [([64], 65544, 64), ([40] * 40, 6200, 128), ([40] * 128, 6200, 120), ([33, 64, 100, 127] * 10, 6200, 1000),
+        ([8] * 8, 6200, 5000), ([1500, 300, 900], 6200, 3000)]
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts,K,N", LONG, ids=lambda v: f"{len(v)}x{v[0]}" if isinstance(v, list) else str(v))
+def test_long_sums_keep_their_digits(counts, K, N, trans):
+    """Positive terms, so that partial sums only grow.  A tensor-core sum of 768 inputs is 48 steps, each cut at two steps of
+    2^-23 of the partial sum at most; after i of them that is i / 48 of the part, within 15% (the terms' spread is 0.7 of
+    their mean): 2 * 24.5 * 1.15 = 57.  Joining P sums rounds at half a step of the sum so far, (P + 1) / 4 (P = 9, or 11 and
+    then 8 CTAs of a cluster: at most 20), the last rounding one more.  One sum over 6200 inputs loses about 160 steps, at either
+    result type, and one over a CTA's 8200 more."""
+    parts, E = 9 if K == 6200 else 20, len(counts)
+    x = (randn((sum(counts), K), F32, 1).abs() + 0.5).to(BF)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    W = (torch.randn((E, N, K) if trans else (E, K, N), generator=g, device="cuda").abs_() + 0.5).to(BF)
+    off = offsets_of(counts)
+    ref = torch.cat([x[r].double() @ (W[e].double().T if trans else W[e].double()) for e, r in segments(counts)])
+    bound = (57 + (parts + 1) / 4 + 1) * SUM_STEP * ref
+    within(moe.grouped_matmul(x, W, off, transpose_w=trans, out_dtype=F32), ref, bound, "fp32")
+    within(moe.grouped_matmul(x, W, off, transpose_w=trans), ref, bound + round_bound(ref + bound, BF), "bf16")
