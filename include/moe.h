@@ -447,7 +447,8 @@ MOE_API moe_status_t moe_grouped_matmul(const moe_matmul_t* m, const int32_t* of
  * with db not NULL the bias gradient db[e,n] = sum_r dy[r,n].  x[rows_cap, ldx] and dy[rows_cap, ldy]
  * are in m->dtype; dW[E,K,N] and db[E,N] are fp32, contiguous, 16-byte aligned, and overwritten: an
  * expert without rows gets zeros.  out_dtype and transpose_w are not used (for a W[E,N,K] pass dy as x
- * and x as dy).  Sums run in a fixed order: the same inputs give the same bits.  Rows, offsets, status,
+ * and x as dy).  Sums run in a fixed order, bf16 rows as above (a sum for every 768 of them, then fp32): the same
+ * inputs give the same bits.  Rows, offsets, status,
  * checks and errors as above, and results must not overlap anything (dW or db = an input or each other is
  * refused); rows_cap = 0 writes zeros.  1 launch, 1 more with db. */
 MOE_API moe_status_t moe_grouped_wgrad(const moe_matmul_t* m, const int32_t* offsets, const void* x, const void* dy,
@@ -550,7 +551,8 @@ MOE_API moe_status_t moe_expert_ffn_q4(const moe_shape_t* shape, const moe_io_t*
 
 /* Kernel-selection switches for side-by-side comparisons of the kernels; normal use needs none.
  *   MOE_KERNEL_NO_CTA_PAIR  single-CTA 128-row grouped-GEMM tiles everywhere, instead of the CTA-pair
- *                           256 x 256 tiles the long-segment shapes use (forward and backward GEMMs)
+ *                           256 x 256 tiles the long-segment shapes use (forward and backward GEMMs).
+ *                           moe_grouped_wgrad then adds its sums of 768 rows in dW itself, at half the speed
  *   MOE_KERNEL_NO_TC_GATE   the CUDA-core gate kernels instead of the tensor-core ones (mma.sync for
  *                           8/16/32 experts, the tcgen05 GEMM for multiples of 64)
  *   MOE_KERNEL_NO_TMA_ROUTER  for bf16 with 8 or 16 experts, the register-direct mma.sync gate (x loaded

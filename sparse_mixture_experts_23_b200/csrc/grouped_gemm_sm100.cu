@@ -32,6 +32,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
+#include <limits.h>
 #include <math.h>
 #include <stdlib.h>
 
@@ -1393,6 +1394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
+  // a caller's rows: a sum of its own for every kSumK of them, which the epilogue adds to what it has written
+  const int part = g.rows_cap > 0 ? kSumK / C::kBK : INT_MAX;
   auto decode = [&](int tile, int& e, int& m0, int& n0) {
     e = tile / per_e;
     const int local = tile - e * per_e;
@@ -1453,7 +1456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int e, m0, n0;
       decode(tile, e, m0, n0);
       const int r0 = offs[e], cnt = offs[e + 1] - r0, KB = (cnt + C::kBK - 1) / C::kBK;
-      const int buf = it & 1;
+      int buf = it & 1, part0 = 0;
       const uint32_t tphase = (uint32_t)((it >> 1) & 1);
       if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(buf), tphase ^ 1u, g.wait_limit, abort_flag, g.status,
                                              kDevTimeoutMma))) {
@@ -1461,8 +1464,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t d_tmem = tmem_base + (uint32_t)(buf * C::kTileN);
+      uint32_t d_tmem = tmem_base + (uint32_t)(buf * C::kTileN);
       for (int kb = 0; kb < KB; ++kb) {
+        if (kb - part0 == part) {
+          // hand this part's sums to the epilogue and go on in the other accumulator
+          if (lane == 0) mma_commit(tfull_bar(buf));
+          __syncwarp();
+          part0 = kb;
+          ++it;
+          buf = it & 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(buf), (uint32_t)((it >> 1) & 1) ^ 1u, g.wait_limit, abort_flag, g.status,
+                                                 kDevTimeoutMma))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          d_tmem = tmem_base + (uint32_t)(buf * C::kTileN);
+        }
         if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, g.wait_limit, abort_flag, g.status,
                                                kDevTimeoutMma))) {
           ok = false;
@@ -1488,7 +1506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < C::kBK / 16; ++kk)
             mma_bf16(d_tmem, desc_mnmajor(a_addr + kk * 16 * 128, C::kBoxBytes),
-                     desc_mnmajor(b_addr + kk * 16 * 128, C::kBoxBytes), C::kIdesc, (kb | kk) != 0 ? 1u : 0u);
+                     desc_mnmajor(b_addr + kk * 16 * 128, C::kBoxBytes), C::kIdesc, kk != 0 || kb != part0 ? 1u : 0u);
           mma_commit(empty_bar(stage));
         }
         issued = true;
@@ -1516,36 +1534,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       int e, m0, n0;
       decode(tile, e, m0, n0);
       const bool empty = offs[e + 1] == offs[e];
-      const int buf = it & 1;
-      const uint32_t tphase = (uint32_t)((it >> 1) & 1);
-      const bool got = mbar_wait(tfull_bar(buf), tphase, g.wait_limit, abort_flag, g.status, kDevTimeoutEpilogue);
-      if (!__all_sync(0xffffffffu, got)) break;
-      tc_fence_after();
+      const int KB = (offs[e + 1] - offs[e] + C::kBK - 1) / C::kBK, parts = KB > part ? (KB + part - 1) / part : 1;
       const int row0 = m0 + quarter * 32;  // this warp's 32 rows of D
       const int nrows = min(32, g.M - row0);
       float* dst = g.out + (size_t)e * g.M * g.N;
       constexpr int kChunks = C::kTileN / 32 / (kEpiWarps / 4);
+      bool got = true;
+      for (int p = 0; p < parts; ++p) {
+        const int buf = (it + p) & 1;
+        got = __all_sync(0xffffffffu, mbar_wait(tfull_bar(buf), (uint32_t)(((it + p) >> 1) & 1), g.wait_limit, abort_flag, g.status,
+                                                kDevTimeoutEpilogue));
+        if (!got) break;
+        tc_fence_after();
 #pragma unroll 1
-      for (int c = half * kChunks; c < (half + 1) * kChunks; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * C::kTileN + c * 32), r);
-        const int col = n0 + c * 32;
-        if (nrows <= 0 || col >= g.N) continue;
-        // transpose through the warp's staging tile so that each store covers 128 contiguous bytes
-        float4* mine = reinterpret_cast<float4*>(stg + lane * kStgStride);
+        for (int c = half * kChunks; c < (half + 1) * kChunks; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * C::kTileN + c * 32), r);
+          const int col = n0 + c * 32;
+          if (nrows <= 0 || col >= g.N) continue;
+          // transpose through the warp's staging tile so that each store covers 128 contiguous bytes
+          float4* mine = reinterpret_cast<float4*>(stg + lane * kStgStride);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          mine[q] = empty ? make_float4(0.f, 0.f, 0.f, 0.f)
-                          : make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                        __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+          for (int q = 0; q < 8; ++q)
+            mine[q] = empty ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                          __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+          __syncwarp();
+          if (col + lane < g.N) {
+            float* to = dst + (size_t)row0 * g.N + col + lane;
+            float before[32];  // what this thread has written, all rows in flight at once
+#pragma unroll
+            for (int i = 0; i < 32; ++i) before[i] = p > 0 && i < nrows ? to[(size_t)i * g.N] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < nrows) to[(size_t)i * g.N] = before[i] + stg[i * kStgStride + lane];
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
         __syncwarp();
-        if (col + lane < g.N)
-          for (int i = 0; i < nrows; ++i) dst[(size_t)(row0 + i) * g.N + col + lane] = stg[i * kStgStride + lane];
-        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty_bar(buf));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tempty_bar(buf));
+      if (!got) break;
+      it += parts - 1;
     }
   }
 
@@ -1584,7 +1615,7 @@ struct WgPairCfg {
   static constexpr int kOffsOff = kMiscOff + 16;
   static constexpr int kStgOff = (kOffsOff + 260 * 4 + 1023) & ~1023;
   static constexpr int kSmemBytes = 1024 + kStgOff + kEpiWarps * kStgWarpBytes;
-  static constexpr int kChunkStages = 6;
+  static constexpr int kChunkStages = kSumK / kStageK;
   static constexpr int kSplitWarps = 8, kBox = 4096;  // SPLIT: epilogue warps, a staging box of 32 x 32 fp32 each
   static constexpr int kSplitThreads = 128 + 32 * kSplitWarps;  // warps 2 and 3 only give their registers away
   static constexpr int kSplitFew = 40, kSplitMany = 232;

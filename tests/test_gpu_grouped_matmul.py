@@ -290,3 +290,28 @@ def test_long_sums_keep_their_digits(counts, K, N, trans):
     bound = (57 + (parts + 1) / 4 + 1) * SUM_STEP * ref
     within(moe.grouped_matmul(x, W, off, transpose_w=trans, out_dtype=F32), ref, bound, "fp32")
     within(moe.grouped_matmul(x, W, off, transpose_w=trans), ref, bound + round_bound(ref + bound, BF), "bf16")
+
+
+@pytest.mark.parametrize("options", [moe.MOE_KERNEL_DEFAULT, moe.MOE_KERNEL_NO_CTA_PAIR])
+def test_wgrad_of_very_many_rows_keeps_its_digits(options):
+    """Positive terms as in test_long_sums_keep_their_digits: 57 steps of 2^-23 for the sums of 768 rows, (P + 1) / 4 for
+    joining P = 86 of them, one for the last.  One sum over the 65541 rows loses more than a thousand."""
+    n, parts = 65541, 86
+    x, dy = (randn((n, 64), F32, 1).abs() + 0.5).to(BF), (randn((n, 264), F32, 2).abs() + 0.5).to(BF)
+    ref = x.double().T @ dy.double()
+    moe.moe_set_kernel_options(options)
+    try:
+        dW = moe.grouped_wgrad(x, dy, offsets_of([0, n, 0]))
+    finally:
+        moe.moe_set_kernel_options(moe.MOE_KERNEL_DEFAULT)
+    assert not dW[0].any() and not dW[2].any()
+    within(dW[1], ref, (57 + (parts + 1) / 4 + 1) * SUM_STEP * ref)
+
+
+def test_wgrad_single_cta_kernel_of_many_rows():
+    """Sums of 768 rows in the kernel without CTA pairs: none, one, an odd and an even number of them, tiles in sequence."""
+    try:
+        moe.moe_set_kernel_options(moe.MOE_KERNEL_NO_CTA_PAIR)
+        check_wgrad([0, 1, 767, 769, 0, 1537, 2305, 768] * 4, 264, 520, BF, bias=False, pad=1, spare=3)
+    finally:
+        moe.moe_set_kernel_options(moe.MOE_KERNEL_DEFAULT)
