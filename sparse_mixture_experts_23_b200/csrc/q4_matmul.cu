@@ -8,8 +8,11 @@
 // the weights as the 16-row operand (c - 8 is exact in bf16) and eight rows of x as the 8-column one, and joins the
 // fp32 accumulator as  acc += s d:  no weight is rounded, and tensor-core sums (which cut) are short.  fp32 rows are
 // split exactly into three bf16 parts (8 bits of the significand each), three products a step.
+// The codes' differences are taken as (c - 8) / 1024: 128 of them at 8 / 1024 are one x at most, so no sum of a group
+// overflows where x is finite, and the result is multiplied back once (both exact; fp32 rows below 2^-110 lose what their
+// third part has below 2^-133, the least of a bf16).
 // Unpacking sets the pace next to the bytes: a turn of the word and one logic instruction make 16 + c of two codes, a
-// subtraction c - 8.  (Taking 24 sum x from the result instead, by one more product with a constant operand for both
+// subtraction c - 8 (all / 1024).  (Taking 24 sum x from the result instead, by one more product with a constant operand for both
 // tiles, measured no faster: the tensor pipe's clocks cost what the subtractions do.)
 // mma.sync rather than tcgen05: at up to 16 rows the product is a small part of what the tensor pipe could do in the
 // time that the weights take, and its register operand is what unpacking produces.
@@ -99,14 +102,15 @@ __device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-// The eight codes of a word (four in each half) as bf16 pairs of c - 8: 0x4180 | c << 3 is 16 + c in bf16, and taking 24
-// away is exact.  One three-input logic instruction a pair, its two constants in registers.
+// The eight codes of a word (four in each half) as bf16 pairs of (c - 8) / 1024: 0x3c80 | c << 3 is (16 + c) / 1024 in bf16,
+// and taking 24 / 1024 away is exact.  One three-input logic instruction a pair, its two constants in registers.
+constexpr float kCodeUnit = 1.f / 1024, kCodeUnits = 1024.f;
 struct Unpack {
   uint32_t mask, magic;
   __nv_bfloat162 off;
   __device__ __forceinline__ Unpack() {
-    asm volatile("mov.b32 %0, 0x00780078;\nmov.b32 %1, 0x41804180;\n" : "=r"(mask), "=r"(magic));
-    off = __halves2bfloat162(__float2bfloat16_rn(24.f), __float2bfloat16_rn(24.f));
+    asm volatile("mov.b32 %0, 0x00780078;\nmov.b32 %1, 0x3c803c80;\n" : "=r"(mask), "=r"(magic));
+    off = __halves2bfloat162(__float2bfloat16_rn(24.f * kCodeUnit), __float2bfloat16_rn(24.f * kCodeUnit));
   }
   __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&a)[4]) const {
 #pragma unroll
@@ -362,7 +366,7 @@ __device__ __forceinline__ void store_piece(const Q4Args& a, const Q4Piece& p, c
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int n = p.pair * 32 + (lane >> 2) + 8 * i;
-      const float v = activate<ACT, sizeof(O) == 2>(sums.v[i >> 1][r >> 1][(i & 1) * 2 + (r & 1)] + b[i]);
+      const float v = activate<ACT, sizeof(O) == 2>(fmaf(sums.v[i >> 1][r >> 1][(i & 1) * 2 + (r & 1)], kCodeUnits, b[i]));
       if (n < a.N) y[n] = (O)v;
     }
   }

@@ -271,3 +271,20 @@ def test_layer_in_4_bits(dtype, act, bias, routing):
     buf.expert_ffn_q4(W1, W2, combine=False)
     buf.combine()
     assert torch.equal(buf.out, fused)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_rows_near_the_largest_number(dtype, group):
+    """Finite rows times small weights are finite: a group's sum before its scale must not overflow."""
+    K, N, rows = 256, 40, 18
+    q, _ = codes_and_scales(1, K, N, group, 3)
+    s = torch.full((1, K // group, N), 2.0 ** -14, dtype=BF, device="cuda")
+    x = (torch.rand((rows, K), device="cuda") * 2e38 + 1e38).to(dtype)
+    x[1::2] *= torch.where(torch.rand((rows // 2, K), device="cuda") < 0.5, -1, 1).to(dtype)
+    x[2] = torch.finfo(dtype).max
+    w = dense(q, s)[0]
+    ref, mag = x.double() @ w, x.double().abs() @ w.abs()
+    assert mag.max() < torch.finfo(dtype).max
+    y = moe.q4_matmul(x, moe.Q4Weights(q, s), offsets_of([rows]), out_dtype=F32)
+    within(y, ref, ((3 if dtype == F32 else 1) * K + 162) * SUM_STEP * mag)
