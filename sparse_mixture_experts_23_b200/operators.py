@@ -6,7 +6,9 @@ what the caller did not pass, and call the C entry point of the same meaning (``
 the current stream of the tensors' device.  Inputs made on another stream have to be ordered before the
 call by the caller, as for any torch operator.  Bad arguments raise ``ValueError``; a status that the library
 returns raises ``MoEError``.  They take part in no autograd graph: gradients are calls of their own, as
-``MoEBuffers.backward`` is.
+``MoEBuffers.backward`` is, and a tensor that requires a gradient is refused while torch records gradients, since its
+gradient would be lost without a word.  Call them under ``torch.no_grad()``, within the forward and backward of a
+``torch.autograd.Function``, or on detached tensors (``q4_quantize`` takes any: codes have no gradient).
 """
 from __future__ import annotations
 
@@ -35,6 +37,11 @@ def _place(t, name: str, index: int) -> None:
     raise ValueError(f"{name} is on {t.device}, expected " + (f"cuda:{index}" if index >= 0 else "cpu"))
 
 
+def _no_graph(name: str) -> None:
+    raise ValueError(f"{name} requires a gradient, which this operator does not record: call it under torch.no_grad() or "
+                     f"with {name}.detach()")
+
+
 def _dtype(t, name: str) -> int:
     code = _CODES.get(t.dtype)
     if code is None:
@@ -46,6 +53,8 @@ def _rows(t, name: str, index: int) -> int:
     """A matrix whose rows are contiguous; returns the elements between them."""
     if t.get_device() != index:
         _place(t, name, index)
+    if t.requires_grad and torch.is_grad_enabled():
+        _no_graph(name)
     strides = t.stride()
     if len(strides) != 2:
         raise ValueError(f"{name} must have two dimensions")
@@ -65,6 +74,8 @@ def _dense(t, name: str, index: int, dtype, shape):
         return None
     if t.get_device() != index:
         _place(t, name, index)
+    if t.requires_grad and torch.is_grad_enabled():
+        _no_graph(name)
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:

@@ -294,3 +294,33 @@ U8, I32 = torch.uint8, torch.int32
 def test_q4_tensor_checks(call, message):
     with pytest.raises(ValueError, match=message):
         call()
+
+
+def leaf(*shape):
+    return z(*shape).requires_grad_()
+
+
+OFF3 = z(3, dtype=I32)
+GRAPH = {
+    "x": lambda: moe.grouped_matmul(leaf(4, 64), z(2, 64, 8), OFF3),
+    "W": lambda: moe.grouped_matmul(z(4, 64), leaf(2, 64, 8), OFF3),
+    "bias": lambda: moe.grouped_matmul(z(4, 64), z(2, 64, 8), OFF3, bias=leaf(2, 8)),
+    "out": lambda: moe.grouped_matmul(z(4, 64), z(2, 64, 8), OFF3, out=leaf(4, 8)),
+    "dy": lambda: moe.grouped_wgrad(z(4, 64), leaf(4, 8), OFF3),
+    "dW": lambda: moe.grouped_wgrad(z(4, 64), z(4, 8), OFF3, dW=z(2, 64, 8, dtype=torch.float32).requires_grad_()),
+    "u": lambda: moe.act_dropout(leaf(4, 8)),
+    "gate": lambda: moe.act_dropout(z(4, 8), gate=leaf(4, 8)),
+    "du": lambda: moe.act_dropout_backward(z(4, 8), z(4, 8), du=leaf(4, 8)),
+    "x of q4": lambda: moe.q4_matmul(leaf(4, 128), q4_weights(), OFF3, ws=z(1)),
+    "bias of q4": lambda: moe.q4_matmul(z(4, 128), q4_weights(), OFF3, bias=leaf(2, 8), ws=z(1)),
+}
+
+
+@pytest.mark.parametrize("name", GRAPH)
+def test_tensors_that_require_a_gradient_are_refused(name):
+    """The operators record no graph: a gradient would be lost silently.  Without grad mode the call goes on."""
+    with pytest.raises(ValueError, match=f"^{name.split()[0]} requires a gradient"):
+        GRAPH[name]()
+    for off in (torch.no_grad(), torch.inference_mode()):
+        with off, pytest.raises(ValueError, match="needs CUDA tensors"):
+            GRAPH[name]()
