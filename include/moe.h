@@ -576,6 +576,13 @@ MOE_API int moe_get_kernel_options(void);
  * pointer with n > 0), MOE_ERR_CUDA.  One launch (none for n = 0). */
 MOE_API moe_status_t moe_debug_activation(int activation, const float* u, float* out, int64_t n, cudaStream_t stream);
 
+/* The kernel that a bf16 moe_grouped_matmul of these sizes takes, with the kernel options as they are: form[0] = 1 for
+ * CTA pairs (256 x 256 tiles); form[1] = output columns of a tile; form[2] = rows of a load box, 0 for a whole tile's
+ * (8: rows spread over the tile); form[3] = CTAs that share a tile's contraction.  For tests that every kernel is
+ * run.  Errors: as moe_grouped_matmul for m, MOE_ERR_INVALID_ARG for form = NULL, MOE_ERR_UNSUPPORTED for fp32 or no rows.
+ * No launch. */
+MOE_API moe_status_t moe_debug_matmul_form(const moe_matmul_t* m, int32_t* form);
+
 /* Launches one block that waits on a pipeline barrier nothing will ever complete, with the
  * current wait bound; it must come back with the error word set.  For testing the timeout path. */
 MOE_API moe_status_t moe_debug_timeout_probe(void* ws, size_t ws_bytes, cudaStream_t stream);

@@ -32,7 +32,7 @@ ENTRY_POINTS = (
     "moe_set_kernel_options", "moe_get_kernel_options", "moe_copy_row_segments", "moe_expert_ffn_rows",
     "moe_expert_ffn_rows_workspace_size", "moe_debug_activation", "moe_grouped_matmul", "moe_grouped_wgrad",
     "moe_act_dropout", "moe_act_dropout_backward", "moe_q4_packed_size", "moe_q4_quantize", "moe_q4_pack",
-    "moe_q4_dequantize", "moe_q4_workspace_size", "moe_q4_matmul", "moe_expert_ffn_q4",
+    "moe_q4_dequantize", "moe_q4_workspace_size", "moe_q4_matmul", "moe_expert_ffn_q4", "moe_debug_matmul_form",
 )
 MOE_KERNEL_DEFAULT, MOE_KERNEL_NO_CTA_PAIR, MOE_KERNEL_NO_TC_GATE, MOE_KERNEL_NO_TMA_ROUTER = 0, 1, 2, 4
 
@@ -168,6 +168,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_expert_ffn_q4.restype = st
     lib.moe_debug_activation.argtypes = [ctypes.c_int, vp, vp, ctypes.c_int64, vp]
     lib.moe_debug_activation.restype = st
+    lib.moe_debug_matmul_form.argtypes = [P(Matmul), P(i32)]
+    lib.moe_debug_matmul_form.restype = st
     lib.moe_debug_timeout_probe.argtypes = [vp, sz, vp]
     lib.moe_debug_timeout_probe.restype = st
     lib.moe_last_launch_count.argtypes = []
@@ -358,6 +360,12 @@ def moe_q4_matmul(m: Q4, offsets, x, packed, bias, y, ws, ws_bytes, stream=0) ->
 def moe_expert_ffn_q4(shape, io, group, W1q, W2q, ws, ws_bytes, combine=1, stream=0) -> int:
     return load_library().moe_expert_ffn_q4(ctypes.byref(shape), ctypes.byref(io), group, W1q, W2q, ws, ws_bytes,
                                             int(combine), stream)
+
+
+def moe_debug_matmul_form(m: Matmul):
+    """(status, (CTA pairs, tile columns, box rows, CTAs a tile)) of a bf16 product."""
+    form = (ctypes.c_int32 * 4)()
+    return load_library().moe_debug_matmul_form(ctypes.byref(m), form), tuple(form)
 
 
 def moe_debug_activation(activation: int, u, out, n: int, stream=0) -> int:

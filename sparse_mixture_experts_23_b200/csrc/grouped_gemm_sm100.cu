@@ -2261,13 +2261,37 @@ cudaError_t launch_split(const CUtensorMap& ma, const CUtensorMap& mb, const CUt
   return cudaLaunchKernelEx(&config, kernel, ma, mb, mas, g);
 }
 
-// The plain grouped product (moe_grouped_matmul).  Tiles as for the FFN's GEMMs: CTA pairs where an expert
-// fills a pair tile on average, else single-CTA tiles with the row placement for short segments.
+// Row tiles at most: the full ones, and a ragged one for each expert that can hold rows.
+static long long most_row_tiles(const GroupedArgs& a, int rows) { return a.rows_cap / rows + (a.rows_cap < a.E ? a.rows_cap : a.E); }
+
+// Tiles as for the FFN's GEMMs: CTA pairs where an expert fills a pair tile on average, else single-CTA tiles with the row
+// placement for short segments.
+RowsForm rows_form(const GroupedArgs& a) {
+  const long long avg = a.rows_cap / a.E;  // rows of an expert, on average
+  const int sms = sm_count();
+  // (pair tiles on less than a quarter of the SMs: the smaller ones below, with K split, are faster: 1 expert of 300 rows,
+  // 8192 x 512, 45 -> 16 us)
+  const long long pair_tiles = most_row_tiles(a, PairCfg::kTileM) * ((a.N + 255) / 256);
+  if (avg >= PairCfg::kTileM && 8 * pair_tiles >= sms && pair_mode_enabled()) return {true, PairCfg::kTileN, 0, 1};
+  // the widest tile that N fills, unless there are fewer tiles than SMs: what one CTA has to bring through its K loop
+  // then sets the time (2 experts of 92 rows in all, 6688 x 192: 83 us at 256 columns, 68 at 64, and 32 with its
+  // rows in one box: a CTA issues a copy in about 64 clocks, and 8-row boxes are up to 16 a step)
+  const long long mt = most_row_tiles(a, BM);
+  int bn = a.N > 128 ? 256 : (a.N > 64 ? 128 : 64);
+  while (bn > 64 && mt * ((a.N + bn - 1) / bn) < sms) bn /= 2;
+  const long long tiles = mt * ((a.N + bn - 1) / bn);
+  const int box_rows = avg < 32 ? 16 : (avg < BM && tiles >= sms ? 8 : 0);
+  // K in 2 to 8 parts of 4 blocks at least where that many more CTAs fit (the same case: 32 -> 11 us)
+  int splits = 1;
+  while (bn == 64 && splits < 8 && 2 * splits * tiles <= sms && (a.K + BK - 1) / BK >= 8 * splits) splits *= 2;
+  return {false, bn, box_rows, splits};
+}
+
+// The plain grouped product (moe_grouped_matmul): one of rows_form's kernels.
 template <int EPI>
 cudaError_t launch_rows(const GroupedArgs& a, cudaStream_t st) {
   const int rows = (int)a.rows_cap;
-  // the experts that can hold rows: with fewer rows than experts, each held one at most on average
-  const long long avg = a.rows_cap / a.E;
+  const RowsForm f = rows_form(a);
   GemmArgs g{};
   g.offsets = a.offsets;
   g.E = a.E;
@@ -2280,51 +2304,29 @@ cudaError_t launch_rows(const GroupedArgs& a, cudaStream_t st) {
   g.ldo = a.ldy;
   g.status = a.status;
   g.wait_limit = wait_limit();
+  g.a_box_rows = f.box_rows;
+  g.spread_rows = f.box_rows == 8;
+  if (f.splits > 1) g.k_splits = f.splits;
   const int grid = sm_count();
   CUtensorMap ma, mb, mas;
   if (!make_map_a(&ma, a.x, rows, a.K, a.ldx)) return cudaErrorInvalidValue;
-  // (pair tiles on less than a quarter of the SMs: the smaller ones below, with K split, are faster: 1 expert of 300 rows,
-  // 8192 x 512, 45 -> 16 us)
-  const long long pair_tiles = (a.rows_cap / PairCfg::kTileM + (a.rows_cap < a.E ? a.rows_cap : a.E)) * ((a.N + 255) / 256);
-  if (avg >= PairCfg::kTileM && 8 * pair_tiles >= grid && pair_mode_enabled()) {
-    const bool ok = a.transpose_w ? make_map_bk(&mb, a.W, a.E, a.N, a.K, PairCfg::kHalfN) : make_map_b(&mb, a.W, a.E, a.K, a.N);
-    if (!ok) return cudaErrorInvalidValue;
-    return a.transpose_w ? launch_pair<EPI, true>(ma, mb, ma, g, grid, st) : launch_pair<EPI>(ma, mb, ma, g, grid, st);
-  }
-  // the widest tile that N fills, unless there are fewer tiles than SMs: what one CTA has to bring through its K loop
-  // then sets the time (2 experts of 92 rows in all, 6688 x 192: 83 us at 256 columns, 68 at 64, and 32 with its
-  // rows in one box: a CTA issues a copy in about 64 clocks, and 8-row boxes are up to 16 a step)
-  const long long mt = a.rows_cap / BM + (a.rows_cap < a.E ? a.rows_cap : a.E);
-  int bn = a.N > 128 ? 256 : (a.N > 64 ? 128 : 64);
-  while (bn > 64 && mt * ((a.N + bn - 1) / bn) < grid) bn /= 2;
-  const bool few = mt * ((a.N + bn - 1) / bn) < grid;
-  const bool small = avg < 32, spread = !small && avg < BM && !few;
-  g.a_box_rows = small ? 16 : (spread ? 8 : 0);
-  g.spread_rows = spread ? 1 : 0;
-  if (g.a_box_rows > 0 && !make_map_a_rows(&mas, a.x, rows, a.K, g.a_box_rows, a.ldx)) return cudaErrorInvalidValue;
-  const CUtensorMap* as = g.a_box_rows > 0 ? &mas : nullptr;
-  // K in 2 to 8 parts of 4 blocks at least where that many more CTAs fit (the same case: 32 -> 11 us)
-  const long long tiles = mt * ((a.N + 63) / 64);
-  int splits = 1;
-  while (bn == 64 && splits < 8 && 2 * splits * tiles <= grid && (a.K + BK - 1) / BK >= 8 * splits) splits *= 2;
-  if (splits > 1) {
-    g.k_splits = splits;
-    if (a.transpose_w) {
-      if (!make_map_bk(&mb, a.W, a.E, a.N, a.K, 64)) return cudaErrorInvalidValue;
-      return launch_split<EPI, true>(ma, mb, as ? mas : ma, g, (int)tiles, st);
-    }
-    if (!make_map_b(&mb, a.W, a.E, a.K, a.N)) return cudaErrorInvalidValue;
-    return launch_split<EPI, false>(ma, mb, as ? mas : ma, g, (int)tiles, st);
+  if (!(a.transpose_w ? make_map_bk(&mb, a.W, a.E, a.N, a.K, f.pair ? PairCfg::kHalfN : f.bn) : make_map_b(&mb, a.W, a.E, a.K, a.N)))
+    return cudaErrorInvalidValue;
+  if (f.box_rows > 0 && !make_map_a_rows(&mas, a.x, rows, a.K, f.box_rows, a.ldx)) return cudaErrorInvalidValue;
+  if (f.pair) return a.transpose_w ? launch_pair<EPI, true>(ma, mb, ma, g, grid, st) : launch_pair<EPI>(ma, mb, ma, g, grid, st);
+  const CUtensorMap* as = f.box_rows > 0 ? &mas : nullptr;
+  if (f.splits > 1) {
+    const int tiles = (int)(most_row_tiles(a, BM) * ((a.N + f.bn - 1) / f.bn));
+    return a.transpose_w ? launch_split<EPI, true>(ma, mb, as ? mas : ma, g, tiles, st)
+                         : launch_split<EPI, false>(ma, mb, as ? mas : ma, g, tiles, st);
   }
   if (a.transpose_w) {
-    if (!make_map_bk(&mb, a.W, a.E, a.N, a.K, bn)) return cudaErrorInvalidValue;
-    if (bn == 256) return launch_one<256, EPI, true>(ma, mb, g, grid, st, as);
-    if (bn == 128) return launch_one<128, EPI, true>(ma, mb, g, grid, st, as);
+    if (f.bn == 256) return launch_one<256, EPI, true>(ma, mb, g, grid, st, as);
+    if (f.bn == 128) return launch_one<128, EPI, true>(ma, mb, g, grid, st, as);
     return launch_one<64, EPI, true>(ma, mb, g, grid, st, as);
   }
-  if (!make_map_b(&mb, a.W, a.E, a.K, a.N)) return cudaErrorInvalidValue;
-  if (bn == 256) return launch_one<256, EPI>(ma, mb, g, grid, st, as);
-  if (bn == 128) return launch_one<128, EPI>(ma, mb, g, grid, st, as);
+  if (f.bn == 256) return launch_one<256, EPI>(ma, mb, g, grid, st, as);
+  if (f.bn == 128) return launch_one<128, EPI>(ma, mb, g, grid, st, as);
   return launch_one<64, EPI>(ma, mb, g, grid, st, as);
 }
 

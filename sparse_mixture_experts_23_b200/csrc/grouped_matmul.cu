@@ -694,6 +694,20 @@ moe_status_t moe_grouped_matmul(const moe_matmul_t* m, const int32_t* offsets, c
   return MOE_OK;
 }
 
+moe_status_t moe_debug_matmul_form(const moe_matmul_t* m, int32_t* form) {
+  moe::GroupedArgs g{};
+  const moe_status_t st = moe::check_matmul(m, false, &g);
+  if (st != MOE_OK) return st;
+  if (form == nullptr) return MOE_ERR_INVALID_ARG;
+  if (m->dtype != MOE_DTYPE_BF16 || m->rows_cap == 0) return MOE_ERR_UNSUPPORTED;
+  const moe::RowsForm f = moe::rows_form(g);
+  form[0] = f.pair;
+  form[1] = f.bn;
+  form[2] = f.box_rows;
+  form[3] = f.splits;
+  return MOE_OK;
+}
+
 moe_status_t moe_grouped_wgrad(const moe_matmul_t* m, const int32_t* offsets, const void* x, const void* dy, float* dW,
                                float* db, int32_t* status, cudaStream_t stream) {
   moe::NvtxRange nvtx_range("moe_grouped_wgrad");

@@ -339,6 +339,13 @@ struct GroupedArgs {
 };
 // Argument rules of the two calls; fills the sizes of g.
 moe_status_t check_matmul(const moe_matmul_t* m, bool wgrad, GroupedArgs* g);
+struct RowsForm {  // how launch_grouped_matmul_sm100 runs a product
+  bool pair;
+  int bn;        // columns of a tile
+  int box_rows;  // of A: 16 for a few rows an expert, 8 with the rows spread, 0 for whole tiles
+  int splits;    // CTAs that share a tile's K
+};
+RowsForm rows_form(const GroupedArgs& a);
 cudaError_t launch_grouped_matmul_sm100(const GroupedArgs& a, cudaStream_t st);
 cudaError_t launch_grouped_wgrad_sm100(const GroupedArgs& a, const void* dy, float* dW, cudaStream_t st);
 

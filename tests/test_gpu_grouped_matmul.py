@@ -315,3 +315,58 @@ def test_wgrad_single_cta_kernel_of_many_rows():
         check_wgrad([0, 1, 767, 769, 0, 1537, 2305, 768] * 4, 264, 520, BF, bias=False, pad=1, spare=3)
     finally:
         moe.moe_set_kernel_options(moe.MOE_KERNEL_DEFAULT)
+
+
+# Shapes that reach every kernel of the bf16 product, as (CTA pairs, tile columns, box rows, CTAs that share K), with ragged N
+# and K.  Those with whole K have more tiles than the GPU has SMs, most of them twice that, so that accumulators and stages
+# are taken again.
+FORMS = [
+    ((1, 256, 0, 1), [1500, 300, 0, 900], 1288, 5000),
+    ((0, 256, 16, 1), [9, 0, 1, 30, 16, 8, 17, 3] * 2, 200, 11000),
+    ((0, 256, 8, 1), [33, 64, 0, 1, 100, 127, 128, 140] * 6, 840, 3000),
+    ((0, 256, 0, 1), [200, 0, 129, 300] * 8, 136, 3000),
+    ((0, 128, 16, 1), [40, 1, 0, 20, 3] * 50 + [4000], 72, 120),
+    ((0, 128, 8, 1), [130, 129, 0, 200, 100] * 51, 72, 120),
+    ((0, 128, 0, 1), [300, 0, 127, 128, 200] * 51, 72, 104),
+    ((0, 64, 16, 1), [40, 1, 0, 20, 3] * 50 + [4000], 72, 56),
+    ((0, 64, 8, 1), [130, 129, 0, 200, 100] * 51, 200, 64),
+    ((0, 64, 0, 1), [300, 0, 127, 128, 200] * 51, 72, 8),
+    ((0, 64, 0, 1), [40] * 40, 520, 120),  # fewer tiles than SMs
+    ((0, 64, 0, 2), [64], 2056, 4040),
+    ((0, 64, 0, 4), [64, 40], 4104, 904),
+    ((0, 64, 0, 8), [100, 7], 7000, 200),
+    ((0, 64, 16, 8), [10, 0, 3], 4104, 72),
+]
+FORM_IDS = ["pair" if f[0] else f"{f[1]}x{f[2]}x{f[3]}x{len(c)}" for f, c, _, _ in FORMS]
+
+
+def form_of(rows, E, K, N, out_dtype, trans):
+    m = moe.Matmul(E, rows, K, N, moe.MOE_DTYPE_BF16, int(out_dtype == BF), int(trans), K, N)
+    status, form = moe.moe_debug_matmul_form(m)
+    assert status == moe.MOE_OK
+    return form
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("form,counts,K,N", FORMS, ids=FORM_IDS)
+def test_every_bf16_kernel(form, counts, K, N, out_dtype, trans):
+    """Against fp64, with a pitch, spare rows and a bias; the dispatch is asked, so that a later rule cannot drop one."""
+    spare = 3
+    assert form_of(sum(counts) + spare, len(counts), K, N, out_dtype, trans) == form
+    check_forward(counts, K, N, BF, out_dtype, trans, bias=True, pad=1, spare=spare, seed=21)
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("trans", [False, True])
+def test_single_cta_kernels_where_pairs_would_run(out_dtype, trans):
+    counts, K, N = [1500, 300, 0, 900], 1288, 1400
+    size = (sum(counts) + 3, len(counts), K, N, out_dtype, trans)
+    assert form_of(*size)[0] == 1
+    check_forward(counts, K, N, BF, out_dtype, trans, bias=True, pad=1, spare=3, seed=22)
+    try:
+        moe.moe_set_kernel_options(moe.MOE_KERNEL_NO_CTA_PAIR)
+        assert form_of(*size)[0] == 0
+        check_forward(counts, K, N, BF, out_dtype, trans, bias=True, pad=1, spare=3, seed=22)
+    finally:
+        moe.moe_set_kernel_options(moe.MOE_KERNEL_DEFAULT)

@@ -324,3 +324,22 @@ def test_tensors_that_require_a_gradient_are_refused(name):
     for off in (torch.no_grad(), torch.inference_mode()):
         with off, pytest.raises(ValueError, match="needs CUDA tensors"):
             GRAPH[name]()
+
+
+def test_matmul_form_query():
+    """The dispatch rule of the bf16 product, for 148 SMs where there is no GPU to ask."""
+    assert moe.moe_debug_matmul_form(matmul(E=0))[0] == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_debug_matmul_form(matmul(K=60))[0] == moe.MOE_ERR_UNSUPPORTED
+    assert moe.moe_debug_matmul_form(matmul(dtype=0, out_dtype=0))[0] == moe.MOE_ERR_UNSUPPORTED
+    assert moe.moe_debug_matmul_form(matmul(rows_cap=0))[0] == moe.MOE_ERR_UNSUPPORTED
+    assert moe.load_library().moe_debug_matmul_form(ctypes.byref(matmul()), None) == moe.MOE_ERR_INVALID_ARG
+    status, form = moe.moe_debug_matmul_form(matmul(E=8, rows_cap=8192, K=4096, N=14336))
+    assert status == moe.MOE_OK and form == (1, 256, 0, 1)
+    try:
+        moe.moe_set_kernel_options(moe.MOE_KERNEL_NO_CTA_PAIR)
+        assert moe.moe_debug_matmul_form(matmul(E=8, rows_cap=8192, K=4096, N=14336)) == (moe.MOE_OK, (0, 256, 0, 1))
+    finally:
+        moe.moe_set_kernel_options(moe.MOE_KERNEL_DEFAULT)
+    assert moe.moe_debug_matmul_form(matmul(E=8, rows_cap=64, K=4096, N=14336))[1] == (0, 256, 16, 1)
+    assert moe.moe_debug_matmul_form(matmul(E=128, rows_cap=8104, K=1024, N=4096))[1] == (0, 256, 8, 1)
+    assert moe.moe_last_launch_count() == 0
