@@ -370,3 +370,11 @@ def test_single_cta_kernels_where_pairs_would_run(out_dtype, trans):
         check_forward(counts, K, N, BF, out_dtype, trans, bias=True, pad=1, spare=3, seed=22)
     finally:
         moe.moe_set_kernel_options(moe.MOE_KERNEL_DEFAULT)
+
+
+def test_wgrad_many_tiles_of_unlike_segments():
+    """384 tiles for 74 pairs of CTAs: empty tiles, tiles of one sum and of an odd and an even number of them follow each
+    other on a pair, whose two accumulators change hands at every sum."""
+    base = [0, 1, 767, 769, 0, 0, 1537, 2305, 768, 5, 0, 130, 1536, 3, 0, 900]
+    check_wgrad(base * 4, 264, 520, BF, bias=True, pad=1, spare=9)
+    check_wgrad(base[::-1] + base, 1032, 264, BF, bias=False)
