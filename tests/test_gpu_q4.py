@@ -288,3 +288,38 @@ def test_rows_near_the_largest_number(dtype, group):
     assert mag.max() < torch.finfo(dtype).max
     y = moe.q4_matmul(x, moe.Q4Weights(q, s), offsets_of([rows]), out_dtype=F32)
     within(y, ref, ((3 if dtype == F32 else 1) * K + 162) * SUM_STEP * mag)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K,N,group", [(14336, 40, 64), (14336, 33, 128), (8224, 24, 32), (14272, 8, 64)])
+@pytest.mark.parametrize("counts", [[1], [8, 0, 9], [17, 1]], ids=lambda c: "-".join(map(str, c)))
+def test_long_sums_that_are_exact(counts, K, N, group, dtype):
+    """Whole inputs up to 15 and scales 1 and 2: every product and every partial sum is a whole number below 2 * 8 * 15 * K <
+    2^22, so that fp32 sums are exact in any order, and a step lost, doubled or taken from its neighbour shows."""
+    E, n = len(counts), sum(counts)
+    q, _ = codes_and_scales(E, K, N, group, K + N)
+    g = torch.Generator().manual_seed(N)
+    s = (torch.randint(0, 2, (E, K // group, N), generator=g) + 1).to(BF).cuda()
+    x = (torch.randint(-15, 16, (n, K), generator=g)).to(dtype).cuda()
+    w = dense(q, s)
+    ref = torch.cat([x[r].double() @ w[e] for e, r in segments(counts)])
+    assert torch.equal(moe.q4_matmul(x, moe.Q4Weights(q, s), offsets_of(counts), out_dtype=F32).double(), ref)
+
+
+def test_long_sums_of_fp32_rows_keep_all_parts():
+    """Rows of whole numbers up to 2^20 - 1, which take all three bf16 parts, against weights of one, minus one and zero: sums
+    below 2^24 by pairing each input with its negative, but for the last two of a group."""
+    K, N, group, rows = 14336, 24, 128, 9
+    g = torch.Generator().manual_seed(1)
+    x = torch.randint(-(2 ** 20) + 1, 2 ** 20, (rows, K // 2), generator=g).double()
+    x = torch.stack([x, -x], 2).view(rows, K)
+    last = torch.arange(K) % (16 * group) >= 16 * group - 2
+    x[:, last] = torch.randint(-(2 ** 20) + 1, 2 ** 20, (rows, int(last.sum())), generator=g).double()
+    pair = torch.randint(7, 10, (1, N, K // 2), generator=g)  # one code for both inputs of a pair: 7, 8 or 9
+    q = (pair | pair << 4).to(torch.uint8).cuda()
+    s = torch.ones((1, K // group, N), dtype=BF, device="cuda")
+    x = x.cuda()
+    ref = x @ dense(q, s)[0]
+    assert ref.abs().max() < 2 ** 24
+    y = moe.q4_matmul(x.float(), moe.Q4Weights(q, s), offsets_of([rows]))
+    assert torch.equal(y.double(), ref)
