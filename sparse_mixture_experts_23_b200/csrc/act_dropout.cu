@@ -8,11 +8,14 @@
 // backward pass computes the same words again.  A dropped element is 0 whatever its inputs hold.
 //
 // Bound: issue slots next to HBM (4099 x 14336 gated bf16 forward and backward: 705 MB, 107 us at the copy rate; 940
-// MB and 143 us as the two calls that both read u and gate).  A vector of 16 bytes (8 bf16 or 4 fp32 columns: whole Philox blocks) of one row per thread and step, the next row's
-// vectors loaded before this one's arithmetic, 24 warps an SM that walk down the rows.  Ten Philox rounds are 20 wide
-// multiplies and 20 three-input xors for four elements; the round keys, the same for all elements, stay in registers.
-// Measured 162 us, 5.8 TB/s (298 us with two rows a thread and short-lived blocks; 174 us with 32 warps an SM, whose 64
-// registers a thread do not hold the keys).  24 and 36 instructions an element forward and backward, ALU pipe at 49%.
+// MB and 143 us as the two calls that both read u and gate).  A vector of 16 bytes (8 bf16 or 4 fp32 columns: whole
+// Philox blocks) of one row per thread and step, the next row's vectors loaded before this one's arithmetic, 24 warps an
+// SM that walk down the rows.  Ten Philox rounds are 20 wide multiplies and 20 three-input xors for four elements; the
+// round keys, the same for all elements, stay in registers.
+// Measured 163 us replayed from a graph, 5.8 TB/s, and 175 to 179 as two calls a step (298 us with two rows a thread and
+// short-lived blocks; 174 us replayed with 32 warps an SM, whose 64 registers a thread do not hold the keys).  24 and 36
+// instructions an element forward and backward, ALU pipe at 49%.  The block fits widths of 2048 bf16 columns: 1408 of
+// them leave 31% of its threads idle.
 // All arithmetic is fp32; each output is rounded once.
 #include <cuda_bf16.h>
 #include <math.h>

@@ -75,7 +75,7 @@ __host__ __device__ constexpr bool epi_dgrad(int epi) { return epi == EPI_DGRAD_
 // its steps of 16: one sum over 14336 inputs is 1.6e-5 off its result, 6.4e-5 where the terms have one sign, and a bf16
 // y's rounding goes the other way for 0.8% to 1.3% of the results.  So the accumulator of every kSumK inputs is a sum of
 // its own, which the epilogue adds into fp32 registers, in order: 7e-7 at any length (the layer's own GEMMs keep one sum).
-// What it costs: nothing to 1% on whole tiles, 0.4 to 1 us of 11 to 18 where a cluster shares K.
+// What it costs: nothing to 3% on whole tiles, 0.4 to 1 us of 11 to 18 where a cluster shares K.
 constexpr int kSumK = 768;
 // Up to 128 columns a thread are held there: two warps a lane quarter for tiles of 256.
 __host__ __device__ constexpr int epi_warps(int epi, int bn) { return epi_rows(epi) && bn == 256 ? 8 : kEpiWarps; }
