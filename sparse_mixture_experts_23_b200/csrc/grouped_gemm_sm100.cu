@@ -11,7 +11,8 @@
 //   moe_grouped_matmul (EPI_ROWS_F32, EPI_ROWS_BF16): the same sum with any N and K that are multiples of 8, rows of
 //   x and y at a pitch of their own, caller-given offsets, and every kSumK inputs summed apart
 //
-// Design (one persistent CTA per SM, 64 + 32 * kEpiWarps threads: 192 with the default 4 epilogue warps):
+// Design (one persistent CTA per SM, 64 + 32 * kEpiWarps threads: 192 with the default 4 epilogue warps, 320 with the 8 of
+// the row products' 256-wide tiles):
 //   warp 0      TMA producer: A tile [128 rows x 64 k] (K-major, 128B swizzle) and B tile
 //               [64 k x BN n] (weights are stored n-contiguous, i.e. MN-major, 128B swizzle, loaded
 //               as BN/64 boxes of 64x64) into a kStages-deep shared-memory ring.
@@ -600,9 +601,9 @@ __device__ __forceinline__ void router_epilogue(const GemmArgs& g, uint32_t tadd
 }
 
 
-// KSPLIT (EPI_ROWS_* only): for fewer tiles than SMs.  A cluster of k_splits CTAs takes one tile, each a part of its K
-// range; then every CTA collects its share of the tile's columns from all of them through distributed shared memory
-// (the stage ring is free by then), adds them in rank order and stores them.
+// KSPLIT (EPI_ROWS_* only): for fewer tiles than SMs.  A cluster of k_splits CTAs takes one tile, each a share of its K
+// range, summed in registers like a whole tile's; then every CTA collects its share of the tile's columns from all of them
+// through distributed shared memory (the stage ring is free by then), adds them in rank order and stores them.
 template <int BN, int EPI, bool BKM, bool KSPLIT = false>
 __global__ void __launch_bounds__(gemm_threads(EPI, BN), 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
